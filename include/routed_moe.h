@@ -61,11 +61,13 @@ typedef struct {
  *                              section 计算公式 step 4: scale = row_max|x| / 127);
  *   MOE_QUANT_NVFP4_G16        group-16 NVFP4 with the global encoding scale qx, the
  *                              layer's input quantization ("Cake SiTU backend", intro; the
- *                              arithmetic is given at moe_quantize_nvfp4). */
+ *                              arithmetic is given at moe_quantize_nvfp4);
+ *   MOE_QUANT_E4M3_ROW_DYNAMIC per-row dynamic E4M3 (scale = row_max|x| / 448). */
 typedef enum {
   MOE_QUANT_NONE = 0,
   MOE_QUANT_INT8_ROW_DYNAMIC = 1,
-  MOE_QUANT_NVFP4_G16 = 2
+  MOE_QUANT_NVFP4_G16 = 2,
+  MOE_QUANT_E4M3_ROW_DYNAMIC = 3   /* moe_rmsnorm and moe_grouped_gemm only */
 } moe_quant_t;
 
 /* Human-readable text of a status code (static storage; never NULL). */
@@ -320,6 +322,93 @@ moe_status_t moe_forward_noalloc(moe_dims_t d, int32_t T, const uint16_t* x,
 moe_status_t moe_topk_softmax(int32_t T, int32_t num_experts, int32_t top_k,
                               const float* logits, int32_t* expert_ids, uint16_t* route_weights,
                               moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The stages of an expert layer whose weights are BF16 or 8 bits wide, one entry point
+ * each: the norm before it, the projection that makes the router's logits, the products by
+ * expert and the weighted sum back into tokens.  With moe_topk_softmax and moe_route /
+ * moe_route_v2 they make the whole layer:
+ *   moe_rmsnorm -> moe_matvec_nvfp4 (logits) -> moe_topk_softmax -> moe_route ->
+ *   moe_grouped_gemm (FC1, SiTU) -> moe_grouped_gemm (FC2) -> moe_combine.
+ * The conventions at the top of this file hold.  None of them needs a workspace, so calls
+ * on different streams only need distinct outputs.
+ * ------------------------------------------------------------------------------------ */
+
+/* Root-mean-square norm with the residual's addition and an output in 8 bits:
+ *   h[t] = x[t] + residual[t]  (x[t] without a residual), in fp32;
+ *   y[t, i] = h[t, i] / sqrt(mean_i(h[t, i]^2) + eps) * weight[i], in fp32;
+ *   residual_out = BF16(h), y = BF16(y);
+ *   q MOE_QUANT_INT8_ROW_DYNAMIC: scales[t] = max_i|y[t, i]| / 127, codes[t, i] =
+ *        clip(round_half_even(y[t, i] / scales[t]), -127, 127);
+ *   q MOE_QUANT_E4M3_ROW_DYNAMIC: scales[t] = max_i|y[t, i]| / 448, codes[t, i] =
+ *        E4M3(y[t, i] / scales[t]), nearest even;
+ * codes are 0 where the scale is 0, and are taken from the fp32 y, not from its BF16
+ * rounding.  A row with a NaN or infinite h has a NaN scale.
+ * Buffers (device): x, residual (or NULL), residual_out (or NULL; needs residual), y (or
+ * NULL) BF16 [T, H]; weight BF16 [H]; codes int8 / E4M3 bytes [T, H] and scales f32 [T]
+ * (both NULL with MOE_QUANT_NONE, else both given).  At least one of y and codes is given.
+ * residual_out and y may be the same buffer as x or residual.  Limits: 1 <= T <= 2^21,
+ * H % 8 == 0, 8 <= H <= 65536, eps >= 0 and finite. */
+moe_status_t moe_rmsnorm(int32_t T, int32_t H, const uint16_t* x, const uint16_t* residual,
+                         const uint16_t* weight, float eps, moe_quant_t q,
+                         uint16_t* residual_out, uint16_t* y, void* codes, float* scales,
+                         moe_stream_t stream);
+
+/* Products of a few token rows with an NVFP4 weight matrix (a projection at decode time, or
+ * the router's logits):
+ *   y[t, n] = alpha * sum_b S[n, b] * sum_{i<16} E2M1(code[n, 16b + i]) * x[t, 16b + i]
+ * accumulated in fp32; no weight is rounded.  codes [N, K/2] and scales [N, K/16] are
+ * moe_quantize_nvfp4's of a BF16 [N, K] matrix (one group, q = 1/alpha), alpha is its
+ * decoding factor.
+ * Buffers (device): x BF16 [T, K]; codes, scales u8; alpha f32 [1]; y BF16 [T, N], or f32
+ * [T, N] with y_is_f32 != 0 (the logits moe_topk_softmax takes).
+ * Limits: 1 <= T <= MOE_MATVEC_MAX_TOKENS, 1 <= N <= 2^20, K % 16 == 0, 16 <= K <= 65536. */
+#define MOE_MATVEC_MAX_TOKENS 64
+moe_status_t moe_matvec_nvfp4(int32_t T, int32_t N, int32_t K, const uint16_t* x,
+                              const uint8_t* codes, const uint8_t* scales, const float* alpha,
+                              void* y, int32_t y_is_f32, moe_stream_t stream);
+
+/* Matrix products grouped by expert.  The R rows are sorted by expert: expert e owns rows
+ * expert_cumsum[e-1] .. expert_cumsum[e] - 1 (the inclusive prefix sums moe_route writes);
+ * rows at and past expert_cumsum[E-1] are left as they were.  With W_e = w[e], [Nw, K]:
+ *   h[i, n] = sum_k X[i, k] * W_e[n, k]
+ *   out[i, n] = BF16(h[i, n]),                     Nw = N   (MOE_EPILOGUE_NONE)
+ *   out[i, n] = BF16(SiTU(h[i, n], h[i, N + n])),  Nw = 2N  (MOE_EPILOGUE_SITU: rows [0, N)
+ *               of W_e are the gate, [N, 2N) the up rows; SiTU as at moe_forward)
+ * X[i] is x[i], or x[row_idx[i] / row_div] when row_idx is given: with sorted_row_idx and
+ * row_div = k the products read the k routed rows of a token from the token itself.  A
+ * source row outside [0, x_rows) counts as zeros.
+ *   q MOE_QUANT_NONE:              x and w BF16, fp32 accumulation;
+ *   q MOE_QUANT_INT8_ROW_DYNAMIC:  x and w int8, h = acc * x_scale[source row] *
+ *        w_scale[e, n] with acc the exact int32 sum (x as moe_route's int8 rows and
+ *        expanded scales, or moe_rmsnorm's);
+ *   q MOE_QUANT_E4M3_ROW_DYNAMIC:  x and w E4M3, acc an fp32 sum, h as for int8.
+ * Buffers (device): x [x_rows, K]; x_scale f32 [x_rows]; w [E, Nw, K]; w_scale f32 [E, Nw]
+ * (both scales NULL with MOE_QUANT_NONE); expert_cumsum i32 [E]; row_idx i32 [R] or NULL
+ * (then x_rows >= R); situ_beta, situ_linear_beta f32 [E] or NULL (4 and 25; NULL without
+ * the SiTU epilogue); out BF16 [R, N], not overlapping x.
+ * Limits: 1 <= R, x_rows <= 2^24, 1 <= N <= 65536, K % 8 == 0 (K % 16 == 0 for 8 bits),
+ * 8 <= K <= 65536, 1 <= E <= 10240, row_div >= 1. */
+typedef enum { MOE_EPILOGUE_NONE = 0, MOE_EPILOGUE_SITU = 1 } moe_epilogue_t;
+
+moe_status_t moe_grouped_gemm(int32_t R, int32_t N, int32_t K, int32_t E, moe_quant_t q,
+                              moe_epilogue_t epilogue, const void* x, const float* x_scale,
+                              int32_t x_rows, const int32_t* row_idx, int32_t row_div,
+                              const int32_t* expert_cumsum, const void* w, const float* w_scale,
+                              const float* situ_beta, const float* situ_linear_beta,
+                              uint16_t* out, moe_stream_t stream);
+
+/* Weighted sum of expert rows back into tokens:
+ *   out[t] = BF16(sum_j route_weights[t, j] * rows[expanded_row_idx[t*k + j]] + add[t])
+ * in fp32, j in order and add last; an index outside [0, R) (a dropped row: -1) is left out.
+ * Buffers (device): rows BF16 [R, H]; expanded_row_idx i32 [T*k] (moe_route's gather map);
+ * route_weights BF16 [T, k]; add BF16 [T, H] (the residual or a shared expert's output) or
+ * NULL; out BF16 [T, H], may be the same buffer as add.
+ * Limits: 1 <= T <= 2^21, T*k <= 2^24, 1 <= R <= 2^24, H % 8 == 0, 8 <= H <= 65536,
+ * 1 <= k <= 64. */
+moe_status_t moe_combine(int32_t T, int32_t H, int32_t k, int32_t R, const uint16_t* rows,
+                         const int32_t* expanded_row_idx, const uint16_t* route_weights,
+                         const uint16_t* add, uint16_t* out, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * Chunk-streamed front end, one rank ("[RFC] Chunk-ready symmetric-buffer protocol for

@@ -19,6 +19,9 @@ __all__ = [
     "MoeRing", "make_ring", "moe_ring_layout", "moe_ring_init", "moe_ring_acquire",
     "moe_ring_publish", "moe_forward_streamed", "moe_sealed_workspace_size",
     "moe_forward_absorb", "moe_forward_seal", "moe_topk_softmax", "moe_forward_noalloc",
+    "moe_rmsnorm", "moe_matvec_nvfp4", "moe_grouped_gemm", "moe_combine",
+    "MOE_MATVEC_MAX_TOKENS", "MOE_EPILOGUE_NONE", "MOE_EPILOGUE_SITU",
+    "MOE_QUANT_E4M3_ROW_DYNAMIC",
     "MOE_NOALLOC_SCRATCH_BYTES", "MOE_RING_ROUTE",
     "MOE_RING_LAYOUT",
     "MOE_RING_OK", "MOE_RING_CONSUMER_TIMEOUT", "MOE_RING_PRODUCER_TIMEOUT",
@@ -32,6 +35,10 @@ library_path = os.path.join(_PKG, "lib", "libroutedmoe.so")
 MOE_QUANT_NONE = 0
 MOE_QUANT_INT8_ROW_DYNAMIC = 1
 MOE_QUANT_NVFP4_G16 = 2
+MOE_QUANT_E4M3_ROW_DYNAMIC = 3
+MOE_EPILOGUE_NONE = 0
+MOE_EPILOGUE_SITU = 1
+MOE_MATVEC_MAX_TOKENS = 64
 MOE_MAX_TOKENS = 16384
 MOE_FORWARD_STAGES = 5
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -43,7 +50,8 @@ EXPORTED = ("moe_status_string", "moe_workspace_size", "moe_prepared_weights_siz
             "moe_forward_timed", "moe_ring_layout", "moe_ring_init", "moe_ring_acquire",
             "moe_ring_publish", "moe_forward_streamed", "moe_sealed_workspace_size",
             "moe_forward_absorb", "moe_forward_seal", "moe_topk_softmax",
-            "moe_forward_noalloc")
+            "moe_forward_noalloc", "moe_rmsnorm", "moe_matvec_nvfp4", "moe_grouped_gemm",
+            "moe_combine")
 
 MOE_RING_ROUTE = 0
 MOE_RING_LAYOUT = 1
@@ -136,6 +144,11 @@ def _lib():
             "moe_forward_absorb": (st, [MoeDims, ctypes.POINTER(MoeRing), I32, I32, I32, P,
                                         ctypes.c_uint32, P, SZ, P]),
             "moe_forward_seal": (st, [MoeDims, I32, P, P, P, P, P, P, P, SZ, P, P]),
+            "moe_rmsnorm": (st, [I32, I32, P, P, P, ctypes.c_float, ctypes.c_int, P, P, P, P, P]),
+            "moe_matvec_nvfp4": (st, [I32, I32, I32, P, P, P, P, P, I32, P]),
+            "moe_grouped_gemm": (st, [I32, I32, I32, I32, ctypes.c_int, ctypes.c_int, P, P, I32, P,
+                                      I32, P, P, P, P, P, P, P]),
+            "moe_combine": (st, [I32, I32, I32, I32, P, P, P, P, P, P]),
             "moe_forward_noalloc": (st, [MoeDims, I32, P, P, P, P, P, P, P, P, P, P, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -341,3 +354,83 @@ def moe_topk_softmax(T, num_experts, top_k, logits, expert_ids, route_weights, s
     _check("moe_topk_softmax", _lib().moe_topk_softmax(
         T, num_experts, top_k, _ptr(logits), _ptr(expert_ids), _ptr(route_weights),
         _stream(stream)))
+
+
+def _checked(fn, stream, *buffers):
+    """Addresses of the buffers, given as (name, tensor, elements, bytes of one element).
+
+    A tensor is looked at before its address is passed on: on one GPU (the current one when
+    the stream is the current stream), contiguous, of that element size and at least that
+    many elements; None and int addresses pass as they are."""
+    device, out = None, []
+    for name, t, n, size in buffers:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: {name} is not on a GPU")
+        if device is None:
+            device = t.get_device()
+            if stream is None:
+                import torch
+                here = torch.cuda.current_device()
+            else:
+                here = device if isinstance(stream, int) else stream.device_index
+            if device != here:
+                raise ValueError(f"{fn}: {name} is on GPU {device}, the stream on GPU {here}")
+        elif t.get_device() != device:
+            raise ValueError(f"{fn}: {name} is on GPU {t.get_device()}, others on GPU {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} is not contiguous")
+        if t.element_size() != size or t.numel() < n:
+            raise ValueError(f"{fn}: {name} holds {t.numel()} elements of {t.element_size()} bytes, "
+                             f"not {n} of {size}")
+        out.append(t.data_ptr())
+    return out
+
+
+def moe_rmsnorm(T, H, x, residual, weight, eps, quant, residual_out, y, codes, scales,
+                stream=None):
+    x, residual, weight, residual_out, y, codes, scales = _checked(
+        "moe_rmsnorm", stream, ("x", x, T * H, 2), ("residual", residual, T * H, 2),
+        ("weight", weight, H, 2), ("residual_out", residual_out, T * H, 2), ("y", y, T * H, 2),
+        ("codes", codes, T * H, 1), ("scales", scales, T, 4))
+    _check("moe_rmsnorm", _lib().moe_rmsnorm(T, H, x, residual, weight, eps, quant, residual_out,
+                                             y, codes, scales, _stream(stream)))
+
+
+def moe_matvec_nvfp4(T, N, K, x, codes, scales, alpha, y, out_f32=False, stream=None):
+    x, codes, scales, alpha, y = _checked(
+        "moe_matvec_nvfp4", stream, ("x", x, T * K, 2), ("codes", codes, N * K // 2, 1),
+        ("scales", scales, N * K // 16, 1), ("alpha", alpha, 1, 4),
+        ("y", y, T * N, 4 if out_f32 else 2))
+    _check("moe_matvec_nvfp4", _lib().moe_matvec_nvfp4(T, N, K, x, codes, scales, alpha, y,
+                                                       int(out_f32), _stream(stream)))
+
+
+def moe_grouped_gemm(R, N, K, E, x, expert_cumsum, w, out, quant=MOE_QUANT_NONE, x_scale=None,
+                     w_scale=None, x_rows=None, row_idx=None, row_div=None, situ=False,
+                     situ_beta=None, situ_linear_beta=None, stream=None):
+    """``x_rows`` defaults to R; ``row_div`` counts with ``row_idx`` only."""
+    x_rows = R if x_rows is None else x_rows
+    row_div = 1 if row_idx is None or row_div is None else row_div
+    size, Nw = 2 if quant == MOE_QUANT_NONE else 1, 2 * N if situ else N
+    x, x_scale, row_idx, expert_cumsum, w, w_scale, situ_beta, situ_linear_beta, out = _checked(
+        "moe_grouped_gemm", stream, ("x", x, x_rows * K, size), ("x_scale", x_scale, x_rows, 4),
+        ("row_idx", row_idx, R, 4), ("expert_cumsum", expert_cumsum, E, 4),
+        ("w", w, E * Nw * K, size), ("w_scale", w_scale, E * Nw, 4),
+        ("situ_beta", situ_beta, E, 4), ("situ_linear_beta", situ_linear_beta, E, 4),
+        ("out", out, R * N, 2))
+    _check("moe_grouped_gemm", _lib().moe_grouped_gemm(
+        R, N, K, E, quant, MOE_EPILOGUE_SITU if situ else MOE_EPILOGUE_NONE, x, x_scale, x_rows,
+        row_idx, row_div, expert_cumsum, w, w_scale, situ_beta, situ_linear_beta, out,
+        _stream(stream)))
+
+
+def moe_combine(T, H, k, R, rows, expanded_row_idx, route_weights, add, out, stream=None):
+    rows, expanded_row_idx, route_weights, add, out = _checked(
+        "moe_combine", stream, ("rows", rows, R * H, 2),
+        ("expanded_row_idx", expanded_row_idx, T * k, 4),
+        ("route_weights", route_weights, T * k, 2), ("add", add, T * H, 2), ("out", out, T * H, 2))
+    _check("moe_combine", _lib().moe_combine(T, H, k, R, rows, expanded_row_idx, route_weights,
+                                             add, out, _stream(stream)))

@@ -17,6 +17,9 @@ constexpr size_t kAlign = 256;
 // parameter expert_num: at most 10240, at most 5120 with the key_value histogram); the
 // whole layer takes at most 4096 experts.
 constexpr int kRouteMaxExperts = 10240, kRouteMaxExpertsKeyValue = 5120;
+// Rows of the norm and of the weighted sum (one workgroup of up to 1024 threads each: the
+// grid stays below 2^32 threads), and rows of the products by expert.
+constexpr int kMaxNormTokens = 1 << 21, kMaxGroupedRows = 1 << 24;
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -811,6 +814,99 @@ moe_status_t moe_topk_softmax(int32_t T, int32_t num_experts, int32_t top_k,
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_topk_softmax(logits, T, num_experts, top_k, expert_ids, route_weights,
                                         reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_rmsnorm(int32_t T, int32_t H, const uint16_t* x, const uint16_t* residual,
+                         const uint16_t* weight, float eps, moe_quant_t q,
+                         uint16_t* residual_out, uint16_t* y, void* codes, float* scales,
+                         moe_stream_t stream) {
+  if (q != MOE_QUANT_NONE && q != MOE_QUANT_INT8_ROW_DYNAMIC && q != MOE_QUANT_E4M3_ROW_DYNAMIC)
+    return MOE_ERR_INVALID_ARG;
+  if (T < 1 || H < 1) return MOE_ERR_INVALID_ARG;
+  if (T > kMaxNormTokens || H % 8 || H > 65536) return MOE_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f) || eps > 3.4e38f) return MOE_ERR_INVALID_ARG;
+  if (!x || !weight || (residual_out && !residual)) return MOE_ERR_INVALID_ARG;
+  const bool quant = q != MOE_QUANT_NONE;
+  if (quant ? (!codes || !scales) : (codes || scales || !y)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+      !aligned(residual_out, 16) || !aligned(y, 16) || !aligned(codes, 8) || !aligned(scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  const NormArgs a{T, H, x, residual, weight, eps, residual_out, y, static_cast<uint8_t*>(codes),
+                   scales, q == MOE_QUANT_E4M3_ROW_DYNAMIC};
+  return hip_status(launch_rmsnorm(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_matvec_nvfp4(int32_t T, int32_t N, int32_t K, const uint16_t* x,
+                              const uint8_t* codes, const uint8_t* scales, const float* alpha,
+                              void* y, int32_t y_is_f32, moe_stream_t stream) {
+  if (T < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (T > MOE_MATVEC_MAX_TOKENS || N > (1 << 20) || K % 16 || K > 65536)
+    return MOE_ERR_UNSUPPORTED;
+  if (!x || !codes || !scales || !alpha || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(alpha, 4) ||
+      !aligned(y, 16))
+    return MOE_ERR_INVALID_ARG;
+  DeviceShape shape;
+  const moe_status_t st = device_shape(&shape);
+  if (st != MOE_OK) return st;
+  const MatvecArgs a{T, N, K, x, codes, scales, alpha,
+                     y_is_f32 ? nullptr : static_cast<uint16_t*>(y),
+                     y_is_f32 ? static_cast<float*>(y) : nullptr, shape.cus};
+  return hip_status(launch_matvec_nvfp4(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm(int32_t R, int32_t N, int32_t K, int32_t E, moe_quant_t q,
+                              moe_epilogue_t epilogue, const void* x, const float* x_scale,
+                              int32_t x_rows, const int32_t* row_idx, int32_t row_div,
+                              const int32_t* expert_cumsum, const void* w, const float* w_scale,
+                              const float* situ_beta, const float* situ_linear_beta,
+                              uint16_t* out, moe_stream_t stream) {
+  if (q != MOE_QUANT_NONE && q != MOE_QUANT_INT8_ROW_DYNAMIC && q != MOE_QUANT_E4M3_ROW_DYNAMIC)
+    return MOE_ERR_INVALID_ARG;
+  if (epilogue != MOE_EPILOGUE_NONE && epilogue != MOE_EPILOGUE_SITU) return MOE_ERR_INVALID_ARG;
+  if (R < 1 || N < 1 || K < 1 || E < 1 || x_rows < 1 || row_div < 1) return MOE_ERR_INVALID_ARG;
+  const bool quant = q != MOE_QUANT_NONE, situ = epilogue == MOE_EPILOGUE_SITU;
+  if (R > kMaxGroupedRows || x_rows > kMaxGroupedRows || N > 65536 || K > 65536 ||
+      K % (quant ? 16 : 8) || E > kRouteMaxExperts)
+    return MOE_ERR_UNSUPPORTED;
+  if (!x || !expert_cumsum || !w || !out) return MOE_ERR_INVALID_ARG;
+  if (quant ? (!x_scale || !w_scale) : (x_scale || w_scale)) return MOE_ERR_INVALID_ARG;
+  if (!situ && (situ_beta || situ_linear_beta)) return MOE_ERR_INVALID_ARG;
+  if (!row_idx && (x_rows < R || row_div != 1)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(x_scale, 4) ||
+      !aligned(w_scale, 4) || !aligned(row_idx, 4) || !aligned(expert_cumsum, 4) ||
+      !aligned(situ_beta, 4) || !aligned(situ_linear_beta, 4))
+    return MOE_ERR_INVALID_ARG;
+  DeviceShape shape;
+  const moe_status_t st = device_shape(&shape);
+  if (st != MOE_OK) return st;
+  GroupedArgs a{};
+  a.R = R; a.N = N; a.Nw = situ ? 2 * N : N; a.E = E;
+  a.KB = K * (quant ? 1 : 2);
+  a.quant = static_cast<int>(q); a.situ = situ;
+  a.x = static_cast<const uint8_t*>(x); a.x_scale = x_scale;
+  a.row_idx = row_idx; a.row_div = row_div; a.x_rows = x_rows;
+  a.cumsum = expert_cumsum;
+  a.w = static_cast<const uint8_t*>(w); a.w_scale = w_scale;
+  a.beta = situ_beta; a.lam = situ_linear_beta;
+  a.out = out;
+  a.cus = shape.cus; a.xcds = shape.xcds;
+  return hip_status(launch_grouped(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_combine(int32_t T, int32_t H, int32_t k, int32_t R, const uint16_t* rows,
+                         const int32_t* expanded_row_idx, const uint16_t* route_weights,
+                         const uint16_t* add, uint16_t* out, moe_stream_t stream) {
+  if (T < 1 || H < 1 || k < 1 || R < 1) return MOE_ERR_INVALID_ARG;
+  if (T > kMaxNormTokens || static_cast<int64_t>(T) * k > (1 << 24) || R > kMaxGroupedRows ||
+      H % 8 || H > 65536 || k > 64)
+    return MOE_ERR_UNSUPPORTED;
+  if (!rows || !expanded_row_idx || !route_weights || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned(rows, 16) || !aligned(expanded_row_idx, 4) || !aligned(route_weights, 2) ||
+      !aligned(add, 16) || !aligned(out, 16))
+    return MOE_ERR_INVALID_ARG;
+  const CombineArgs a{T, R, H, k, rows, expanded_row_idx, route_weights, add, out};
+  return hip_status(launch_combine(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

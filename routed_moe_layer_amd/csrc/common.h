@@ -42,6 +42,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
+// One fp32 value to BF16 bits by the hardware conversion (a NaN stays a NaN).
+__device__ __forceinline__ uint16_t f32_to_bf16(float f) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+}
+
 // fp32 value of an E4M3 byte (the byte's sign is ignored: block scales are >= 0).
 // gfx950's fp8 conversion is the OCP E4M3 ("fn") format.
 __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
@@ -118,6 +123,24 @@ __device__ __forceinline__ f16x8 decode8(uint32_t w, f16x2 scale2, float one = 1
   r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
   r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
   return r;
+}
+
+// Dot product of 16 E2M1 values (w, element i in nibble i) with 16 BF16 values (x0, x1),
+// accumulated in fp32: E2M1 values are exact in BF16.  (The words pass through a function
+// argument: a bit cast of a vector element itself reads element 0.)
+__device__ __forceinline__ bf16x2 as_bf16x2(uint32_t w) { return __builtin_bit_cast(bf16x2, w); }
+__device__ __forceinline__ float e2m1_dot8(uint32_t c, u32x4 x, float d) {
+  d = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 0),
+                                      as_bf16x2(x[0]), d, false);
+  d = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 1),
+                                      as_bf16x2(x[1]), d, false);
+  d = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 2),
+                                      as_bf16x2(x[2]), d, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 3),
+                                         as_bf16x2(x[3]), d, false);
+}
+__device__ __forceinline__ float e2m1_dot16(u32x2 w, u32x4 x0, u32x4 x1) {
+  return e2m1_dot8(w[1], x1, e2m1_dot8(w[0], x0, 0.0f));
 }
 
 __device__ __forceinline__ f16x2 scale_f16x2(uint32_t e4m3_byte) {

@@ -171,6 +171,71 @@ hipError_t launch_slot_ids(int32_t* dst, const int32_t* src, int64_t n, const ui
 hipError_t launch_topk_softmax(const float* logits, int64_t T, int E, int k, int32_t* ids,
                                uint16_t* weights, hipStream_t stream);
 
+// Root-mean-square norm with the residual's addition (norm.hip).
+struct NormArgs {
+  int64_t T;
+  int H;                       // a multiple of 8
+  const uint16_t* x;           // [T, H] BF16
+  const uint16_t* res;         // [T, H] or null
+  const uint16_t* weight;      // [H]
+  float eps;
+  uint16_t* res_out;           // [T, H] x + res, or null
+  uint16_t* y;                 // [T, H] or null
+  uint8_t* codes;              // [T, H] int8 or E4M3, or null
+  float* scales;               // [T]
+  int e4m3;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+
+// Few token rows times an NVFP4 matrix (matvec.hip).
+struct MatvecArgs {
+  int T, N, K;                 // K a multiple of 16
+  const uint16_t* x;           // [T, K] BF16
+  const uint8_t* codes;        // [N, K/2]
+  const uint8_t* scales;       // [N, K/16] E4M3
+  const float* alpha;          // [1]
+  uint16_t* y;                 // [T, N] BF16, or
+  float* y_f32;                // [T, N] fp32
+  int cus;
+};
+hipError_t launch_matvec_nvfp4(const MatvecArgs& a, hipStream_t stream);
+
+// Products grouped by expert (grouped.hip).
+struct GroupedArgs {
+  int R, N, Nw, E;             // sorted rows, output columns, weight rows per expert, experts
+  int KB;                      // bytes of K, a multiple of 16
+  int quant;                   // moe_quant_t: 0 BF16, 1 int8, 3 E4M3
+  int situ;
+  const uint8_t* x;            // [x_rows, KB]
+  const float* x_scale;        // [x_rows] (8-bit operands)
+  const int32_t* row_idx;      // [R] row_div * source row + something below row_div, or null
+  int row_div, x_rows;
+  const int32_t* cumsum;       // [E] inclusive
+  const uint8_t* w;            // [E, Nw, KB]
+  const float* w_scale;        // [E, Nw] (8-bit operands)
+  const float* beta;           // [E] or null
+  const float* lam;            // [E] or null
+  uint16_t* out;               // [R, N] BF16
+  int cus, xcds;
+};
+hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
+// Upper bound of the number of row tiles of R rows over E experts, BM rows each.
+inline int64_t max_grouped_tiles(int64_t R, int64_t E, int64_t BM) {
+  return R / BM + (R < E ? R : E);
+}
+
+// Weighted sum of expert rows into tokens (combine.hip).
+struct CombineArgs {
+  int64_t T, R;
+  int H, k;                    // H a multiple of 8
+  const uint16_t* rows;        // [R, H] BF16
+  const int32_t* idx;          // [T * k], outside [0, R): left out
+  const uint16_t* weights;     // [T, k] BF16
+  const uint16_t* add;         // [T, H] or null
+  uint16_t* out;               // [T, H]
+};
+hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
+
 hipError_t launch_prepare_weights(int H, int I, int E, const uint8_t* w13,
                                   const uint8_t* w13_sf, const uint8_t* w2,
                                   const uint8_t* w2_sf, uint8_t* prepared, hipStream_t stream);
