@@ -104,6 +104,20 @@ __device__ __forceinline__ TileRows find_tile(const GroupedArgs& a, const int32_
   return TileRows{e, row0, min(BM, r.y - row0)};
 }
 
+// The same with an expert's rows dealt evenly to its tiles in multiples of 16 (so none is
+// nearly empty while others are full); the last tiles of an expert may hold no row.
+template <int BM>
+__device__ __forceinline__ TileRows find_tile_even(const GroupedArgs& a, const int32_t* s_tile,
+                                                   int tile) {
+  TileRows t = find_tile<BM>(a, s_tile, tile);
+  const int2 r = expert_rows(a, t.expert);
+  const int cnt = r.y - r.x, nt = (cnt + BM - 1) / BM;
+  const int per = ((cnt + nt - 1) / nt + 15) / 16 * 16;
+  t.row0 = r.x + (tile - s_tile[t.expert]) * per;
+  t.nrows = min(per, r.y - t.row0);
+  return t;
+}
+
 // Row of x that sorted row i reads, or -1 (zeros) when the index points outside x.
 __device__ __forceinline__ int64_t source_row(const GroupedArgs& a, int i) {
   int s = i;

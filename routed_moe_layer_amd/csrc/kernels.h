@@ -219,10 +219,6 @@ struct GroupedArgs {
   int cus, xcds;
 };
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
-// Upper bound of the number of row tiles of R rows over E experts, BM rows each.
-inline int64_t max_grouped_tiles(int64_t R, int64_t E, int64_t BM) {
-  return R / BM + (R < E ? R : E);
-}
 
 // Weighted sum of expert rows into tokens (combine.hip).
 struct CombineArgs {
