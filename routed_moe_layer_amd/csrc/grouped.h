@@ -39,8 +39,7 @@ __device__ __forceinline__ typename AccOf<Q>::type mma_chunk(u32x4 a0, u32x4 a1,
       x[i] = static_cast<int>(a0[i]); x[4 + i] = static_cast<int>(a1[i]);
       y[i] = static_cast<int>(b0[i]); y[4 + i] = static_cast<int>(b1[i]);
     }
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, 0x7F7F7F7F, 0,
-                                                           0x7F7F7F7F);   // scales 2^0
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, 0, 0, 0);   // unscaled
   }
   return acc;
 }
@@ -52,10 +51,10 @@ __device__ __forceinline__ int2 expert_rows(const GroupedArgs& a, int e) {
   return make_int2(lo, hi);
 }
 
-// s_tile[e] = number of tiles (of up to BM rows) of the experts before e, s_tile[E] the
-// total.  Every thread of the workgroup calls this; it ends with a barrier.
-template <int BM, int NW>
-__device__ __forceinline__ void scan_tiles(const GroupedArgs& a, int32_t* s_tile) {
+// s[e] = sum of count(rows of expert) over the experts before e, s[E] the total.  Every
+// thread of the workgroup (NW wavefronts) calls this; it ends with a barrier.
+template <int NW, class F>
+__device__ __forceinline__ void scan_experts(const GroupedArgs& a, int32_t* s, F count) {
   __shared__ int32_t s_wave[NW];
   constexpr int kThreads = NW * 64;
   const int per = (a.E + kThreads - 1) / kThreads;
@@ -63,8 +62,8 @@ __device__ __forceinline__ void scan_tiles(const GroupedArgs& a, int32_t* s_tile
   int sum = 0;
   for (int e = lo; e < hi; ++e) {
     const int2 r = expert_rows(a, e);
-    const int n = (r.y - r.x + BM - 1) / BM;
-    s_tile[e] = n;
+    const int n = count(r.y - r.x);
+    s[e] = n;
     sum += n;
   }
   int inc = sum;
@@ -79,44 +78,137 @@ __device__ __forceinline__ void scan_tiles(const GroupedArgs& a, int32_t* s_tile
   int before = inc - sum;
   for (int i = 0; i < wave; ++i) before += s_wave[i];
   for (int e = lo; e < hi; ++e) {
-    const int n = s_tile[e];
-    s_tile[e] = before;
+    const int n = s[e];
+    s[e] = before;
     before += n;
   }
-  if (threadIdx.x == kThreads - 1) s_tile[a.E] = before;
+  if (threadIdx.x == kThreads - 1) s[a.E] = before;
   __syncthreads();
 }
 
 struct TileRows {
   int expert, row0, nrows;
 };
-// The tile's expert (the last one that starts at or before it) and rows; 0 <= tile < s_tile[E].
-template <int BM>
-__device__ __forceinline__ TileRows find_tile(const GroupedArgs& a, const int32_t* s_tile, int tile) {
-  int lo = 0, hi = a.E;                  // s_tile[lo] <= tile < s_tile[hi]
+// The expert of tile `tile`: the last one whose tiles start at or before it; s as from
+// scan_experts, 0 <= tile < s[E].
+__device__ __forceinline__ int tile_expert(const int32_t* s, int E, int tile) {
+  int lo = 0, hi = E;                    // s[lo] <= tile < s[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (s_tile[mid] <= tile) lo = mid; else hi = mid;
+    if (s[mid] <= tile) lo = mid; else hi = mid;
   }
-  const int e = __builtin_amdgcn_readfirstlane(lo);
-  const int2 r = expert_rows(a, e);
-  const int row0 = r.x + (tile - s_tile[e]) * BM;
-  return TileRows{e, row0, min(BM, r.y - row0)};
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// The same with an expert's rows dealt evenly to its tiles in multiples of 16 (so none is
-// nearly empty while others are full); the last tiles of an expert may hold no row.
+// Tiles of up to BM rows with an expert's rows dealt evenly to them in multiples of 16 (so
+// none is nearly empty while others are full); the last tiles of an expert may hold no row.
 template <int BM>
 __device__ __forceinline__ TileRows find_tile_even(const GroupedArgs& a, const int32_t* s_tile,
                                                    int tile) {
-  TileRows t = find_tile<BM>(a, s_tile, tile);
-  const int2 r = expert_rows(a, t.expert);
+  const int e = tile_expert(s_tile, a.E, tile);
+  const int2 r = expert_rows(a, e);
   const int cnt = r.y - r.x, nt = (cnt + BM - 1) / BM;
   const int per = ((cnt + nt - 1) / nt + 15) / 16 * 16;
-  t.row0 = r.x + (tile - s_tile[t.expert]) * per;
-  t.nrows = min(per, r.y - t.row0);
-  return t;
+  const int row0 = r.x + (tile - s_tile[e]) * per;
+  return TileRows{e, row0, min(per, r.y - row0)};
 }
+
+// The work items of a persistent workgroup: an item is a tile and one block of weight rows.
+// Items come in runs of kTileRun tiles (tiles of one expert read the same weights), inside a
+// run by weight block, inside a block by tile.  An XCD works on whole runs, so an item's
+// neighbours share its L2: with many runs they are dealt to the XCDs in turn (popular experts
+// may lie next to each other), with few (below kDealRuns per XCD) each XCD takes an equal
+// contiguous part of all items.  blockIdx.x counts XCDs first; gridDim.x is a multiple of
+// their number.
+constexpr int kTileRun = 4, kDealRuns = 8;
+struct ItemWalk {
+  const GroupedArgs& a;
+  const int32_t* s_tile;
+  int nblk, tiles, xcd, step;
+  bool deal;
+  int64_t at, end;
+  __device__ __forceinline__ ItemWalk(const GroupedArgs& args, const int32_t* tile_starts, int blocks)
+      : a(args), s_tile(tile_starts), nblk(blocks), tiles(tile_starts[args.E]) {
+    xcd = static_cast<int>(blockIdx.x) % a.xcds;
+    step = static_cast<int>(gridDim.x) / a.xcds;
+    at = static_cast<int>(blockIdx.x) / a.xcds;
+    const int runs = (tiles + kTileRun - 1) / kTileRun;
+    deal = runs >= kDealRuns * a.xcds;
+    if (deal) {
+      end = static_cast<int64_t>((runs - xcd + a.xcds - 1) / a.xcds) * kTileRun * nblk;
+    } else {
+      const int64_t total = static_cast<int64_t>(tiles) * nblk;
+      end = total * (xcd + 1) / a.xcds;
+      at += total * xcd / a.xcds;
+    }
+  }
+  // The next item with rows; false when there is none left.
+  template <int BM>
+  __device__ __forceinline__ bool next(TileRows* tr, int* cb) {
+    const int per_run = kTileRun * nblk;               // N <= 65536: below 2^17
+    while (at < end) {
+      int run = static_cast<int>(at / per_run);
+      const int rem = static_cast<int>(at - static_cast<int64_t>(run) * per_run);
+      at += step;
+      if (deal) run = run * a.xcds + xcd;
+      const int in_run = min(kTileRun, tiles - run * kTileRun);
+      if (rem >= in_run * nblk) continue;              // the last run may be short
+      *cb = rem / in_run;
+      *tr = find_tile_even<BM>(a, s_tile, run * kTileRun + rem % in_run);
+      if (tr->nrows > 0) return true;
+    }
+    return false;
+  }
+};
+
+// The same for tiles of BM rows that all cost the same, and one smaller tile per expert for
+// the rest of its rows: the full tiles are dealt first, in equal contiguous parts to the XCDs
+// and one by one to an XCD's workgroups, then the smaller ones, starting with the workgroups
+// that got fewer of the full ones.
+template <int BM>
+struct FullFirstWalk {
+  const GroupedArgs& a;
+  const int32_t *s_full, *s_part;        // prefix sums of the full and the smaller tiles
+  int nblk, step, slot, xcd;
+  bool part = false;
+  int64_t at, end;
+  __device__ __forceinline__ FullFirstWalk(const GroupedArgs& args, const int32_t* full,
+                                           const int32_t* smaller, int blocks)
+      : a(args), s_full(full), s_part(smaller), nblk(blocks) {
+    xcd = static_cast<int>(blockIdx.x) % a.xcds;
+    step = static_cast<int>(gridDim.x) / a.xcds;
+    slot = static_cast<int>(blockIdx.x) / a.xcds;
+    range(s_full[a.E], slot);
+  }
+  __device__ __forceinline__ void range(int tiles, int first) {
+    const int64_t total = static_cast<int64_t>(tiles) * nblk;
+    at = total * xcd / a.xcds;
+    end = total * (xcd + 1) / a.xcds;
+    at += first;
+  }
+  __device__ __forceinline__ bool next(TileRows* tr, int* cb) {
+    if (at >= end && !part) {
+      part = true;
+      // (at - end) % step: this workgroup's place behind those that the last round left out
+      range(s_part[a.E], static_cast<int>((at - end) % step));
+    }
+    if (at >= end) return false;
+    const int32_t* s = part ? s_part : s_full;
+    const int per_run = kTileRun * nblk;
+    const int run = static_cast<int>(at / per_run);
+    const int rem = static_cast<int>(at - static_cast<int64_t>(run) * per_run);
+    const int in_run = min(kTileRun, s[a.E] - run * kTileRun);
+    const int tile = run * kTileRun + rem % in_run;
+    at += step;
+    *cb = rem / in_run;
+    const int e = tile_expert(s, a.E, tile);
+    const int2 r = expert_rows(a, e);
+    const int full = (r.y - r.x) / BM;
+    *tr = part ? TileRows{e, r.x + full * BM, r.y - r.x - full * BM}
+               : TileRows{e, r.x + (tile - s[e]) * BM, BM};
+    return true;
+  }
+};
 
 // Row of x that sorted row i reads, or -1 (zeros) when the index points outside x.
 __device__ __forceinline__ int64_t source_row(const GroupedArgs& a, int i) {
@@ -149,42 +241,92 @@ __device__ __forceinline__ float situ_f32(float g, float u, float beta, float in
   return (beta * tanh_f32(g * inv_beta) * sig) * (lam * tanh_f32(u * inv_lam));
 }
 
-// One lane's four output columns n0 .. n0 + 3 of one token row: scales, activation, one
-// rounding to BF16.  h: the (gate) products, u: the up products of the same columns (SiTU).
-template <int Q, bool SITU>
-__device__ __forceinline__ void store4(const GroupedArgs& a, int e, int n0,
-                                       typename AccOf<Q>::type h, typename AccOf<Q>::type u,
-                                       float xs, uint16_t* orow) {
-  float v[4];
-  float beta = 4.0f, lam = 25.0f;
-  if constexpr (SITU) {
-    if (a.beta) beta = a.beta[e];
-    if (a.lam) lam = a.lam[e];
-  }
-  const float ib = 1.0f / beta, il = 1.0f / lam;
-  const int64_t wrow = static_cast<int64_t>(e) * a.Nw;
+// A lane's share of a finished tile: its output columns, in groups of four, of M token rows.
+// Scales, activation, one rounding to BF16.
+template <int Q, bool SITU, int C, int M>
+struct Epilogue {
+  const GroupedArgs& a;
+  int n0[C];                             // first column of each group
+  float ws[C][4], us[C][4];              // column scales (us: the up columns with SiTU)
+  int row[M];                            // output row, or -1 (not stored)
+  float xs[M];                           // row scale
+  bool there[M];                         // the row has a source (zeros are stored otherwise)
+  float beta, lam, ib, il;
+
+  __device__ __forceinline__ Epilogue(const GroupedArgs& args) : a(args) {}
+  // Everything from memory up front: cols(c) is the first column of group c, rows(m) the
+  // output row of token m, or -1.
+  template <class Cols, class Rows>
+  __device__ __forceinline__ void begin(int expert, Cols cols, Rows rows) {
+    int64_t src[M];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = min(n0 + i, a.N - 1);
-    float hv = static_cast<float>(h[i]);
-    if constexpr (Q != 0) hv = hv * xs * a.w_scale[wrow + n];
-    if constexpr (SITU) {
-      float uv = static_cast<float>(u[i]);
-      if constexpr (Q != 0) uv = uv * xs * a.w_scale[wrow + a.N + n];
-      hv = situ_f32(hv, uv, beta, ib, lam, il);
+    for (int m = 0; m < M; ++m) {
+      row[m] = rows(m);
+      src[m] = row[m] < 0 ? -1 : source_row(a, row[m]);
     }
-    v[i] = hv;
-  }
-  if (n0 + 4 <= a.N && a.N % 4 == 0) {
-    uint2 o;
-    o.x = pack_bf16x2(v[0], v[1]);
-    o.y = pack_bf16x2(v[2], v[3]);
-    *reinterpret_cast<uint2*>(orow + n0) = o;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n0 + i < a.N) orow[n0 + i] = f32_to_bf16(v[i]);
+    for (int m = 0; m < M; ++m) {
+      there[m] = src[m] >= 0;
+      xs[m] = Q == 0 ? 1.0f : a.x_scale[there[m] ? src[m] : 0];
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      n0[c] = cols(c);
+      if constexpr (Q != 0) {
+        const float* w = a.w_scale + static_cast<int64_t>(expert) * a.Nw;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = min(n0[c] + i, a.N - 1);
+          ws[c][i] = w[n];
+          if constexpr (SITU) us[c][i] = w[a.N + n];
+        }
+      }
+    }
+    if constexpr (SITU) {
+      beta = a.beta ? a.beta[expert] : 4.0f;
+      lam = a.lam ? a.lam[expert] : 25.0f;
+      ib = 1.0f / beta;
+      il = 1.0f / lam;
+    }
   }
-}
+  // Columns of group c of token m: h the (gate) products, u the up products (SiTU).
+  __device__ __forceinline__ uint2 columns(int c, int m, typename AccOf<Q>::type h,
+                                           typename AccOf<Q>::type u) const {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = static_cast<float>(h[i]);
+      if constexpr (Q != 0) v[i] = v[i] * xs[m] * ws[c][i];
+      if constexpr (SITU) {
+        float uv = static_cast<float>(u[i]);
+        if constexpr (Q != 0) uv = uv * xs[m] * us[c][i];
+        v[i] = situ_f32(v[i], uv, beta, ib, lam, il);
+      }
+      if (!there[m]) v[i] = 0.0f;
+    }
+    return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+  // Store group c, or the adjacent groups c and c + 1.
+  __device__ __forceinline__ void store(int c, int m, uint2 v) const {
+    uint16_t* o = a.out + static_cast<int64_t>(row[m]) * a.N + n0[c];
+    if (a.N % 4 == 0 && n0[c] + 4 <= a.N) {
+      *reinterpret_cast<uint2*>(o) = v;
+    } else {
+      const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n0[c] + i < a.N) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+  __device__ __forceinline__ void store(int c, int m, uint2 lo, uint2 hi) const {
+    if (a.N % 8 == 0 && n0[c] + 8 <= a.N) {
+      *reinterpret_cast<u32x4*>(a.out + static_cast<int64_t>(row[m]) * a.N + n0[c]) =
+          u32x4{lo.x, lo.y, hi.x, hi.y};
+    } else {
+      store(c, m, lo);
+      store(c + 1, m, hi);
+    }
+  }
+};
 
 }  // namespace rmoe

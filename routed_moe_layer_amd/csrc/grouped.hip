@@ -26,7 +26,6 @@ using acc_t = typename AccOf<Q>::type;
 // ---------------------------------------------------------------------------------------
 constexpr int kMidRows = 128, kMidWaves = 4, kMidThreads = kMidWaves * 64, kMidWR = 2;
 constexpr int kMidStageBytes = 16384;
-constexpr int kTileRun = 4;              // consecutive tiles kept on one XCD
 
 template <int Q, bool SITU, int MT>
 __device__ __forceinline__ void mid_tile(const GroupedArgs& a, const TileRows& tr, int cb,
@@ -50,12 +49,11 @@ __device__ __forceinline__ void mid_tile(const GroupedArgs& a, const TileRows& t
   }
   // this thread's pieces of a stage: row q / kPieces, piece q % kPieces, q = tid + 256 i
   const uint8_t* xp[PPT];
-  bool xok[PPT];
 #pragma unroll
   for (int i = 0; i < PPT; ++i) {
     const int row = (tid + kMidThreads * i) / kPieces;
-    const int64_t src = row < tr.nrows ? source_row(a, tr.row0 + row) : -1;
-    xok[i] = src >= 0;
+    // rows that are not there read the first of the tile; the epilogue leaves them out
+    const int64_t src = source_row(a, tr.row0 + (row < tr.nrows ? row : 0));
     xp[i] = a.x + (src < 0 ? 0 : src) * KB + (tid % kPieces) * 16;
   }
   u32x4 xr[PPT], wv[kDepth][WR][2];
@@ -64,7 +62,7 @@ __device__ __forceinline__ void mid_tile(const GroupedArgs& a, const TileRows& t
 #pragma unroll
     for (int i = 0; i < PPT; ++i) {
       xr[i] = u32x4{0, 0, 0, 0};
-      if (xok[i] && off + (tid % kPieces) * 16 < KB)
+      if (off + (tid % kPieces) * 16 < KB)
         xr[i] = *reinterpret_cast<const u32x4*>(xp[i] + off);
     }
   };
@@ -131,21 +129,16 @@ __device__ __forceinline__ void mid_tile(const GroupedArgs& a, const TileRows& t
       }
     }
   }
+  constexpr int C = SITU ? WR / 2 : WR;
+  Epilogue<Q, SITU, C, MT> out(a);
+  out.begin(tr.expert, [&](int c) { return c0 + 16 * c + 4 * g; },
+            [&](int m) { return 16 * m + l16 < tr.nrows ? tr.row0 + 16 * m + l16 : -1; });
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    if (16 * m + l16 >= tr.nrows) continue;
-    const int i = tr.row0 + 16 * m + l16;
-    uint16_t* orow = a.out + static_cast<int64_t>(i) * a.N;
-    float xs = 1.0f;
-    if constexpr (Q != 0) {
-      const int64_t src = source_row(a, i);
-      if (src >= 0) xs = a.x_scale[src];
-    }
+    if (out.row[m] < 0) continue;
 #pragma unroll
-    for (int r = 0; r < WR; r += SITU ? 2 : 1) {
-      const int n0 = c0 + 16 * (SITU ? r >> 1 : r) + 4 * g;
-      store4<Q, SITU>(a, tr.expert, n0, acc[r][m], acc[SITU ? r + 1 : r][m], xs, orow);
-    }
+    for (int c = 0; c < C; ++c)
+      out.store(c, m, out.columns(c, m, acc[SITU ? 2 * c : c][m], acc[SITU ? 2 * c + 1 : c][m]));
   }
 }
 
@@ -153,24 +146,13 @@ template <int Q, bool SITU>
 __global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(GroupedArgs a) {
   extern __shared__ int32_t s_tile[];
   __shared__ alignas(16) uint8_t stage[2 * kMidStageBytes];
-  scan_tiles<kMidRows, kMidWaves>(a, s_tile);
+  scan_experts<kMidWaves>(a, s_tile, [](int n) { return (n + kMidRows - 1) / kMidRows; });
   constexpr int kCols = kMidWaves * kMidWR * 16 / (SITU ? 2 : 1);
   const int nblk = (a.N + kCols - 1) / kCols;
-  const int tiles = s_tile[a.E];
-  // XCD x takes runs of kTileRun consecutive tiles (tiles of one expert read the same
-  // weights) and all their weight blocks (which read the same rows)
-  const int xcd = static_cast<int>(blockIdx.x) % a.xcds, slot = static_cast<int>(blockIdx.x) / a.xcds;
-  const int slots = static_cast<int>(gridDim.x) / a.xcds;
-  const int64_t per_run = static_cast<int64_t>(kTileRun) * nblk;
-  for (int64_t l = slot;; l += slots) {
-    const int64_t run = l / per_run * a.xcds + xcd;
-    if (run * kTileRun >= tiles) break;
-    const int rem = static_cast<int>(l % per_run);
-    const int tile = static_cast<int>(run * kTileRun) + rem % kTileRun;
-    if (tile >= tiles) continue;
-    const TileRows tr = find_tile_even<kMidRows>(a, s_tile, tile);
-    const int cb = rem / kTileRun;
-    if (tr.nrows <= 0) continue;
+  ItemWalk walk(a, s_tile, nblk);
+  TileRows tr;
+  int cb;
+  while (walk.next<kMidRows>(&tr, &cb)) {
     const int mt = (tr.nrows + 15) / 16;
     if (mt <= 1) mid_tile<Q, SITU, 1>(a, tr, cb, stage);
     else if (mt <= 2) mid_tile<Q, SITU, 2>(a, tr, cb, stage);
@@ -188,11 +170,207 @@ static hipError_t launch_mid(const GroupedArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------------------
+// Tiles of up to 256 rows for experts with many rows.  A workgroup of eight wavefronts
+// multiplies 256 token rows with 256 weight rows, 128 x 64 per wavefront; both operands go
+// from memory straight into LDS, one chunk of 128 bytes of K ahead, and are read as MFMA
+// fragments from there.
+// ---------------------------------------------------------------------------------------
+constexpr int kBigTile = 256, kBigWaves = 8, kBigThreads = kBigWaves * 64;
+constexpr int kBigOperandBytes = kBigTile * 128;
+
+// Sixteen zero bytes: what a lane loads in the place of rows and columns that are not there.
+__device__ const u32x4 g_zero16 = {0u, 0u, 0u, 0u};
+
+typedef const __attribute__((address_space(1))) void* global_ptr;
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// The wave's 64 x 16 bytes from each lane's address into consecutive LDS bytes.
+__device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)dst, 16, 0, 0);
+}
+
+template <int Q, bool SITU>
+__global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs a) {
+  extern __shared__ int32_t s_tile[];                  // two prefix sums of E + 1
+  __shared__ alignas(16) uint8_t s_w0[kBigOperandBytes], s_x0[kBigOperandBytes];
+  __shared__ alignas(16) uint8_t s_w1[kBigOperandBytes], s_x1[kBigOperandBytes];
+  scan_experts<kBigWaves>(a, s_tile, [](int n) { return n / kBigTile; });
+  scan_experts<kBigWaves>(a, s_tile + a.E + 1, [](int n) { return n % kBigTile != 0 ? 1 : 0; });
+  constexpr int kCols = kBigTile / (SITU ? 2 : 1);
+  const int nblk = (a.N + kCols - 1) / kCols;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int g = lane >> 4, l16 = lane & 15;
+  // the wave's weight quarter and token half (the two waves of a SIMD have different halves)
+  const int wn = wave & 3, wm = wave >> 2;
+  const int KB = a.KB, nc = (KB + 127) / 128;
+  const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
+  FullFirstWalk<kBigTile> walk(a, s_tile, s_tile + a.E + 1, nblk);
+
+  // Load side: load j of a wave fills rows 32 wave + 8 j + lane / 8 of both operands, slot
+  // lane % 8 of a row holding piece (lane % 8) ^ (row % 8): the eight rows that a fragment
+  // read touches together fall on different banks.
+  const uint8_t *wp[4], *xp[4];
+  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;
+  TileRows ld;
+  int ld_cb = 0, ld_c = 0;
+  auto begin_item = [&]() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 32 * wave + 8 * j + (lane >> 3);
+      // Row 64 q + 16 r + m holds the weights of MFMA row m of group r of the waves with
+      // wn = q.  The order is chosen for the lanes' accumulators, four rows m = 4 g .. 4 g + 3
+      // of each group: groups 2 s and 2 s + 1 make eight consecutive columns 32 s + 8 g + ...,
+      // with SiTU groups 0 and 2 (gate) and 1 and 3 (up) columns 8 g + ....
+      const int q = row >> 6, r = (row >> 4) & 3, m = row & 15;
+      int n, up = 0;
+      if (SITU) {
+        n = ld_cb * kCols + 32 * q + 8 * (m >> 2) + 4 * (r >> 1) + (m & 3);
+        up = r & 1;
+      } else {
+        n = ld_cb * kCols + 64 * q + 32 * (r >> 1) + 8 * (m >> 2) + 4 * (r & 1) + (m & 3);
+      }
+      n = min(n, a.N - 1) + (up ? a.N : 0);
+      wp[j] = a.w + (static_cast<int64_t>(ld.expert) * a.Nw + n) * KB + piece;
+      // rows that are not there read the first of the tile; the epilogue leaves them out
+      const int64_t src = source_row(a, ld.row0 + (row < ld.nrows ? row : 0));
+      xp[j] = a.x + (src < 0 ? 0 : src) * KB + piece;
+    }
+  };
+  auto load = [&](uint8_t* sw, uint8_t* sx) {
+    const int off = 128 * ld_c;
+    const bool in = off + piece < KB;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_to_lds(in ? wp[j] + off : zero, sw + (32 * wave + 8 * j) * 128);
+    if (32 * wave < ld.nrows) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load_to_lds(in ? xp[j] + off : zero, sx + (32 * wave + 8 * j) * 128);
+    }
+  };
+  // The loads of the chunk after the one that was loaded last: the item's next, or the first
+  // of the next item.  (An item has an even number of chunks, a last one of zeros where K has
+  // an odd one, so that items start with the first buffers.)
+  const int even = nc + (nc & 1);
+  bool more = walk.next(&ld, &ld_cb);
+  if (!more) return;
+  auto load_next = [&](uint8_t* sw, uint8_t* sx) {
+    if (++ld_c == even) {
+      ld_c = 0;
+      more = walk.next(&ld, &ld_cb);
+      if (more) begin_item();
+    }
+    if (more) load(sw, sx);
+  };
+
+  // One item whose rows fit 32 MG tokens; a wave has 16 MG of them.
+  auto item = [&](auto mg_c) {
+    constexpr int MG = decltype(mg_c)::value;
+    const int t0 = 16 * MG * wm;
+    acc_t<Q> acc[4][MG];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int m = 0; m < MG; ++m) acc[r][m] = acc_t<Q>{0, 0, 0, 0};
+    auto compute = [&](const uint8_t* sw, const uint8_t* sx) {
+      u32x4 wf[4][2], xf[2][2];
+      auto read_x = [&](int m) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          xf[m & 1][f] = *reinterpret_cast<const u32x4*>(
+              sx + (t0 + 16 * m + l16) * 128 + (((4 * f + g) ^ (l16 & 7)) << 4));
+      };
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          wf[r][f] = *reinterpret_cast<const u32x4*>(
+              sw + (64 * wn + 16 * r + l16) * 128 + (((4 * f + g) ^ (l16 & 7)) << 4));
+      read_x(0);
+#pragma unroll
+      for (int m = 0; m < MG; ++m) {
+        if (m < MG - 1) read_x(m + 1);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[r][m] = mma_chunk<Q>(wf[r][0], wf[r][1], xf[m & 1][0], xf[m & 1][1], acc[r][m]);
+      }
+      if constexpr (MG == 8) {
+        // issue order: the first reads, then each token group's reads one group ahead
+        constexpr int kMfma = Q == 3 ? 4 : 8;
+        __builtin_amdgcn_sched_group_barrier(0x100, 12, 0);
+#pragma unroll
+        for (int m = 0; m < 6; ++m) {
+          __builtin_amdgcn_sched_group_barrier(0x008, kMfma, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 2 * kMfma, 0);
+      }
+    };
+    const TileRows tr = ld;
+    const int cb = ld_cb;
+    for (int c = 0; c < even; c += 2) {
+      load_next(s_w1, s_x1);
+      compute(s_w0, s_x0);
+      __builtin_amdgcn_s_waitcnt(0);                   // this wave's loads are in LDS
+      __syncthreads();
+      load_next(s_w0, s_x0);
+      compute(s_w1, s_x1);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+    }
+    constexpr int C = SITU ? 2 : 4;
+    Epilogue<Q, SITU, C, MG> out(a);
+    out.begin(
+        tr.expert,
+        [&](int n) {
+          return cb * kCols + 8 * g + (SITU ? 32 * wn + 4 * n : 64 * wn + 32 * (n >> 1) + 4 * (n & 1));
+        },
+        [&](int m) {
+          const int t = t0 + 16 * m + l16;
+          return t < tr.nrows ? tr.row0 + t : -1;
+        });
+#pragma unroll
+    for (int m = 0; m < MG; ++m) {
+      if (out.row[m] < 0) continue;
+#pragma unroll
+      for (int n = 0; n < C; n += 2)
+        out.store(n, m,
+                  out.columns(n, m, acc[SITU ? 2 * n : n][m], acc[SITU ? 2 * n + 1 : n][m]),
+                  out.columns(n + 1, m, acc[SITU ? 2 * n + 2 : n + 1][m],
+                              acc[SITU ? 2 * n + 3 : n + 1][m]));
+    }
+  };
+
+  begin_item();
+  load(s_w0, s_x0);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  while (more) {
+    if (ld.nrows > 128) item(IntC<8>{});
+    else if (ld.nrows > 64) item(IntC<4>{});
+    else if (ld.nrows > 32) item(IntC<2>{});
+    else item(IntC<1>{});
+  }
+}
+
+template <int Q, bool SITU>
+static hipError_t launch_big(const GroupedArgs& a, hipStream_t stream) {
+  const unsigned grid = static_cast<unsigned>(a.cus / a.xcds * a.xcds);
+  grouped_big_kernel<Q, SITU><<<dim3(grid), dim3(kBigThreads),
+                                (static_cast<size_t>(a.E) + 1) * 8, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int Q, bool SITU>
+static hipError_t launch_one(const GroupedArgs& a, hipStream_t stream) {
+  if (a.E <= 1024 && a.R >= a.E * 256) return launch_big<Q, SITU>(a, stream);
+  return launch_mid<Q, SITU>(a, stream);
+}
+
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream) {
   switch (a.quant) {
-    case 0: return a.situ ? launch_mid<0, true>(a, stream) : launch_mid<0, false>(a, stream);
-    case 1: return a.situ ? launch_mid<1, true>(a, stream) : launch_mid<1, false>(a, stream);
-    default: return a.situ ? launch_mid<3, true>(a, stream) : launch_mid<3, false>(a, stream);
+    case 0: return a.situ ? launch_one<0, true>(a, stream) : launch_one<0, false>(a, stream);
+    case 1: return a.situ ? launch_one<1, true>(a, stream) : launch_one<1, false>(a, stream);
+    default: return a.situ ? launch_one<3, true>(a, stream) : launch_one<3, false>(a, stream);
   }
 }
 
