@@ -357,55 +357,70 @@ def moe_topk_softmax(T, num_experts, top_k, logits, expert_ids, route_weights, s
 
 
 def _checked(fn, stream, *buffers):
-    """Addresses of the buffers, given as (name, tensor, elements, bytes of one element).
+    """The stream's handle and the addresses of the buffers, which are given as
+    (name, tensor, elements, bytes of one element).
 
-    A tensor is looked at before its address is passed on: on one GPU (the current one when
-    the stream is the current stream), contiguous, of that element size and at least that
+    A tensor is looked at before its address is passed on: on the stream's GPU (the current
+    one unless the stream says otherwise), contiguous, of that element size and at least that
     many elements; None and int addresses pass as they are."""
-    device, out = None, []
+    device, out = None, [None]
     for name, t, n, size in buffers:
         if t is None or isinstance(t, int):
             out.append(t)
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: {name} is not on a GPU")
-        if device is None:
-            device = t.get_device()
-            if stream is None:
-                import torch
-                here = torch.cuda.current_device()
-            else:
-                here = device if isinstance(stream, int) else stream.device_index
-            if device != here:
-                raise ValueError(f"{fn}: {name} is on GPU {device}, the stream on GPU {here}")
-        elif t.get_device() != device:
-            raise ValueError(f"{fn}: {name} is on GPU {t.get_device()}, others on GPU {device}")
+        at = t.get_device()                    # -1 on the host
+        if at != device:
+            if at < 0:
+                raise ValueError(f"{fn}: {name} is not on a GPU")
+            if device is not None:
+                raise ValueError(f"{fn}: {name} is on GPU {at}, others on GPU {device}")
+            device = at
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} is not contiguous")
         if t.element_size() != size or t.numel() < n:
             raise ValueError(f"{fn}: {name} holds {t.numel()} elements of {t.element_size()} bytes, "
                              f"not {n} of {size}")
         out.append(t.data_ptr())
+    out[0] = _stream_on(fn, stream, device)
     return out
+
+
+def _stream_on(fn, stream, device):
+    """The handle of a stream, which has to be on the GPU of the tensors (device) if any: the
+    library launches on the current GPU."""
+    if stream is None and device is None:
+        return _stream(None)
+    if device is not None:
+        import torch
+        if torch.cuda.current_device() != device:
+            raise ValueError(f"{fn}: the tensors are on GPU {device}, the current one is GPU "
+                             f"{torch.cuda.current_device()}")
+        if stream is None:
+            # torch.cuda.current_stream() without the stream object it makes on the way
+            return torch._C._cuda_getCurrentRawStream(device)
+        if not isinstance(stream, int) and stream.device_index != device:
+            raise ValueError(f"{fn}: the tensors are on GPU {device}, the stream on GPU "
+                             f"{stream.device_index}")
+    return _stream(stream)
 
 
 def moe_rmsnorm(T, H, x, residual, weight, eps, quant, residual_out, y, codes, scales,
                 stream=None):
-    x, residual, weight, residual_out, y, codes, scales = _checked(
+    stream, x, residual, weight, residual_out, y, codes, scales = _checked(
         "moe_rmsnorm", stream, ("x", x, T * H, 2), ("residual", residual, T * H, 2),
         ("weight", weight, H, 2), ("residual_out", residual_out, T * H, 2), ("y", y, T * H, 2),
         ("codes", codes, T * H, 1), ("scales", scales, T, 4))
     _check("moe_rmsnorm", _lib().moe_rmsnorm(T, H, x, residual, weight, eps, quant, residual_out,
-                                             y, codes, scales, _stream(stream)))
+                                             y, codes, scales, stream))
 
 
 def moe_matvec_nvfp4(T, N, K, x, codes, scales, alpha, y, out_f32=False, stream=None):
-    x, codes, scales, alpha, y = _checked(
+    stream, x, codes, scales, alpha, y = _checked(
         "moe_matvec_nvfp4", stream, ("x", x, T * K, 2), ("codes", codes, N * K // 2, 1),
         ("scales", scales, N * K // 16, 1), ("alpha", alpha, 1, 4),
         ("y", y, T * N, 4 if out_f32 else 2))
     _check("moe_matvec_nvfp4", _lib().moe_matvec_nvfp4(T, N, K, x, codes, scales, alpha, y,
-                                                       int(out_f32), _stream(stream)))
+                                                       int(out_f32), stream))
 
 
 def moe_grouped_gemm(R, N, K, E, x, expert_cumsum, w, out, quant=MOE_QUANT_NONE, x_scale=None,
@@ -415,7 +430,8 @@ def moe_grouped_gemm(R, N, K, E, x, expert_cumsum, w, out, quant=MOE_QUANT_NONE,
     x_rows = R if x_rows is None else x_rows
     row_div = 1 if row_idx is None or row_div is None else row_div
     size, Nw = 2 if quant == MOE_QUANT_NONE else 1, 2 * N if situ else N
-    x, x_scale, row_idx, expert_cumsum, w, w_scale, situ_beta, situ_linear_beta, out = _checked(
+    (stream, x, x_scale, row_idx, expert_cumsum, w, w_scale, situ_beta, situ_linear_beta,
+     out) = _checked(
         "moe_grouped_gemm", stream, ("x", x, x_rows * K, size), ("x_scale", x_scale, x_rows, 4),
         ("row_idx", row_idx, R, 4), ("expert_cumsum", expert_cumsum, E, 4),
         ("w", w, E * Nw * K, size), ("w_scale", w_scale, E * Nw, 4),
@@ -424,13 +440,13 @@ def moe_grouped_gemm(R, N, K, E, x, expert_cumsum, w, out, quant=MOE_QUANT_NONE,
     _check("moe_grouped_gemm", _lib().moe_grouped_gemm(
         R, N, K, E, quant, MOE_EPILOGUE_SITU if situ else MOE_EPILOGUE_NONE, x, x_scale, x_rows,
         row_idx, row_div, expert_cumsum, w, w_scale, situ_beta, situ_linear_beta, out,
-        _stream(stream)))
+        stream))
 
 
 def moe_combine(T, H, k, R, rows, expanded_row_idx, route_weights, add, out, stream=None):
-    rows, expanded_row_idx, route_weights, add, out = _checked(
+    stream, rows, expanded_row_idx, route_weights, add, out = _checked(
         "moe_combine", stream, ("rows", rows, R * H, 2),
         ("expanded_row_idx", expanded_row_idx, T * k, 4),
         ("route_weights", route_weights, T * k, 2), ("add", add, T * H, 2), ("out", out, T * H, 2))
     _check("moe_combine", _lib().moe_combine(T, H, k, R, rows, expanded_row_idx, route_weights,
-                                             add, out, _stream(stream)))
+                                             add, out, stream))

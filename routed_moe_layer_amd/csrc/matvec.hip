@@ -1,47 +1,89 @@
 // Products of a few BF16 token rows with an NVFP4 weight matrix (codes and E4M3 block scales
 // as moe_quantize_nvfp4 writes them, one fp32 factor alpha):
 //   y[t, n] = alpha * sum_b S[n, b] * (sum_{i < 16} E2M1(W[n, 16b + i]) * x[t, 16b + i]).
-// An E2M1 value is exact in BF16, so the inner sum is a BF16 dot product accumulated in fp32
-// and the block scale multiplies it in fp32: no weight is rounded.
-//
-// HBM-bound on the 9/16 byte per weight.
+// Bound by the 9/16 byte per weight.  Two kernels: with one or two tokens a wavefront takes
+// whole weight rows, with more the matrix units take 16 tokens at a time.
 #include "common.h"
 #include "kernels.h"
 
 namespace rmoe {
 
-// A wavefront computes RW consecutive weight rows for TT tokens; lane l holds block
-// 64c + l of every row (16 codes: 8 bytes, one scale byte) and the 16 token values of that
-// block, so each load instruction of a row covers 512 contiguous bytes.
-template <int RW, int TT>
-__global__ __launch_bounds__(256) void matvec_kernel(MatvecArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int n0 = (static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x >> 6)) * RW;
-  const int t0 = static_cast<int>(blockIdx.y) * TT;
-  if (n0 >= a.N) return;                                // whole wavefronts; no barrier follows
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------------------------------------
+// One or two tokens.  A wavefront computes RW consecutive weight rows; lane l holds block
+// 64c + l of every row (8 bytes of codes, one scale byte), so a load instruction covers 512
+// contiguous bytes of a row, and the codes of the next kDotDepth steps are on their way while
+// a step is multiplied.  An E2M1 value is exact in BF16: the inner sum is a BF16 dot product accumulated
+// in fp32, multiplied by the block scale in fp32.  The tokens lie in LDS (read once per
+// workgroup; every wavefront reading them from the caches moved as many bytes as the
+// weights), a block's two 16-byte halves in two planes so that the lanes' reads are
+// consecutive.
+// ---------------------------------------------------------------------------------------
+constexpr int kDotDepth = 4, kDotLdsBytes = 65536;
+
+template <int RW, int TT, int NW, bool LDS>
+__global__ __launch_bounds__(NW * 64) void matvec_dot_kernel(MatvecArgs a) {
+  extern __shared__ u32x4 s_x[];                       // [TT][2][K / 16]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n0 = (static_cast<int>(blockIdx.x) * NW + wave) * RW;
   const int nb = a.K / 16;
+  const u32x4* xg = reinterpret_cast<const u32x4*>(a.x);
+  const u32x2* wp[RW];
+  const uint8_t* sp[RW];
+#pragma unroll
+  for (int r = 0; r < RW; ++r) {
+    const int64_t n = min(n0 + r, a.N - 1);             // rows past the end: the last one again
+    wp[r] = reinterpret_cast<const u32x2*>(a.codes) + n * nb;
+    sp[r] = a.scales + n * nb;
+  }
+  u32x2 w[kDotDepth][RW];
+  uint32_t s[kDotDepth][RW];
+  auto load = [&](int u, int b) {
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      w[u][r] = u32x2{0, 0};
+      s[u][r] = 0;
+      if (b < nb) {
+        w[u][r] = __builtin_nontemporal_load(wp[r] + b);
+        s[u][r] = sp[r][b];
+      }
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kDotDepth; ++u) load(u, lane + 64 * u);
+  if constexpr (LDS) {
+    for (int i = threadIdx.x; i < a.T * nb * 2; i += NW * 64) {
+      const int t = i / (2 * nb), h = i - t * 2 * nb;    // half h & 1 of the token's block h / 2
+      s_x[(2 * t + (h & 1)) * nb + (h >> 1)] = xg[i];
+    }
+    __syncthreads();
+  }
+  if (n0 >= a.N) return;                                // whole wavefronts; no barrier follows
   float acc[RW][TT];
 #pragma unroll
   for (int r = 0; r < RW; ++r)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[r][t] = 0.0f;
-  for (int b = lane; b < nb; b += 64) {
-    u32x2 w[RW];
-    uint32_t s[RW];
+  for (int b0 = lane; b0 - lane < nb; b0 += 64 * kDotDepth) {
 #pragma unroll
-    for (int r = 0; r < RW; ++r) {
-      const int64_t n = min(n0 + r, a.N - 1);           // rows past the end: the last one again
-      w[r] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(a.codes) + n * nb + b);
-      s[r] = a.scales[n * nb + b];
-    }
+    for (int u = 0; u < kDotDepth; ++u) {
+      const int b = b0 + 64 * u;
+      if (b - lane >= nb) break;                        // uniform
+      const int bx = min(b, nb - 1);                    // (lanes past the row: zero codes)
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int64_t tt = min(t0 + t, a.T - 1);
-      const u32x4* xp = reinterpret_cast<const u32x4*>(a.x + tt * a.K) + 2 * b;
-      const u32x4 x0 = xp[0], x1 = xp[1];
+      for (int t = 0; t < TT; ++t) {
+        const int tt = min(t, a.T - 1);
+        const u32x4 x0 = LDS ? s_x[2 * tt * nb + bx] : xg[(static_cast<int64_t>(tt) * nb + bx) * 2];
+        const u32x4 x1 =
+            LDS ? s_x[(2 * tt + 1) * nb + bx] : xg[(static_cast<int64_t>(tt) * nb + bx) * 2 + 1];
 #pragma unroll
-      for (int r = 0; r < RW; ++r)
-        acc[r][t] = __builtin_fmaf(e4m3_to_f32(s[r]), e2m1_dot16(w[r], x0, x1), acc[r][t]);
+        for (int r = 0; r < RW; ++r) {
+          const float d = e2m1_dot16(w[u][r], x0, x1);
+          acc[r][t] = __builtin_fmaf(e4m3_to_f32(s[u][r]), b < nb ? d : 0.0f, acc[r][t]);
+        }
+      }
+      load(u, b + 64 * kDotDepth);
     }
   }
   const float alpha = a.alpha[0];
@@ -52,22 +94,186 @@ __global__ __launch_bounds__(256) void matvec_kernel(MatvecArgs a) {
       float v = acc[r][t];
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-      if (lane == 0 && n0 + r < a.N && t0 + t < a.T) {
-        const int64_t o = static_cast<int64_t>(t0 + t) * a.N + n0 + r;
+      if (lane == 0 && n0 + r < a.N && t < a.T) {
+        const int64_t o = static_cast<int64_t>(t) * a.N + n0 + r;
         if (a.y_f32) a.y_f32[o] = v * alpha;
         else a.y[o] = f32_to_bf16(v * alpha);
       }
     }
 }
 
-hipError_t launch_matvec_nvfp4(const MatvecArgs& a, hipStream_t stream) {
-#define RMOE_MATVEC(RW, TT) \
-  matvec_kernel<RW, TT><<<dim3((a.N + 4 * RW - 1) / (4 * RW), (a.T + TT - 1) / TT), dim3(256), 0, stream>>>(a)
-  if (a.T == 1) RMOE_MATVEC(2, 1);
-  else if (a.T == 2) RMOE_MATVEC(2, 2);
-  else RMOE_MATVEC(2, 4);
-#undef RMOE_MATVEC
+// ---------------------------------------------------------------------------------------
+// More tokens, 16 TT at a time.  A workgroup takes 16 G weight rows; its wavefronts share K in
+// chunks of 128 and add their partial sums through LDS in a fixed order at the end, so few
+// rows already fill the chip.  A lane holds 32 consecutive codes of a row (two blocks) and the
+// same 32 values of a token: four 16x16x32 BF16 products, K permuted alike in both operands.
+// A code times its block scale has at most 6 significant bits: exact in BF16.
+// ---------------------------------------------------------------------------------------
+// Eight codes (a word) times a block scale, as a BF16 MFMA operand.
+__device__ __forceinline__ bf16x8 e2m1_scaled8(uint32_t w, float s) {
+  u32x4 r;
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+  const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+  const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+  r[0] = pack_bf16x2(a[0] * s, a[1] * s);
+  r[1] = pack_bf16x2(b[0] * s, b[1] * s);
+  r[2] = pack_bf16x2(c[0] * s, c[1] * s);
+  r[3] = pack_bf16x2(d[0] * s, d[1] * s);
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// PAIRS: K is a multiple of 32, so a lane's two blocks are there or not together and its
+// loads are 16 and 2 bytes wide; else each block is looked at by itself.
+template <int G, int TT, int NW, bool PAIRS>
+__global__ __launch_bounds__(NW * 64) void matvec_mfma_kernel(MatvecArgs a) {
+  constexpr int kRows = 16 * G, kStride = kRows + 4;    // floats per token of a partial sum
+  __shared__ alignas(16) float red[NW][16 * TT][kStride];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int n0 = static_cast<int>(blockIdx.x) * kRows, t0 = static_cast<int>(blockIdx.y) * 16 * TT;
+  const int nb = a.K / 16, nc = (a.K + 127) / 128;
+  const uint8_t *wp[G], *sp[G];
+  const uint16_t* xp[TT];
+#pragma unroll
+  for (int r = 0; r < G; ++r) {
+    const int64_t n = min(n0 + 16 * r + l16, a.N - 1);  // rows past the end: the last one again
+    wp[r] = a.codes + n * (a.K / 2) + 16 * g;
+    sp[r] = a.scales + n * nb + 2 * g;
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+    xp[t] = a.x + static_cast<int64_t>(min(t0 + 16 * t + l16, a.T - 1)) * a.K + 32 * g;
+  f32x4 acc[G][TT];
+#pragma unroll
+  for (int r = 0; r < G; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+  // the next chunk's codes are loaded ahead, and its token values too while they fit
+  constexpr int kXDepth = TT <= 2 ? 2 : 1;
+  u32x4 w[2][G], xv[kXDepth][TT][4];
+  uint32_t s[2][G];
+  auto load_w = [&](int u, int c) {
+    const int k = 128 * c + 32 * g;
+#pragma unroll
+    for (int r = 0; r < G; ++r) {
+      w[u][r] = u32x4{0, 0, 0, 0};
+      s[u][r] = 0;
+      if constexpr (PAIRS) {
+        if (k < a.K) {
+          w[u][r] = *reinterpret_cast<const u32x4*>(wp[r] + 64 * c);
+          s[u][r] = *reinterpret_cast<const uint16_t*>(sp[r] + 8 * c);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (k + 16 * h < a.K) {
+            const u32x2 v = *reinterpret_cast<const u32x2*>(wp[r] + 64 * c + 8 * h);
+            w[u][r][2 * h] = v[0];
+            w[u][r][2 * h + 1] = v[1];
+            s[u][r] |= static_cast<uint32_t>(sp[r][8 * c + h]) << (8 * h);
+          }
+      }
+    }
+  };
+  auto load_x = [&](int u, int c) {
+    const int k = 128 * c + 32 * g;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        xv[u][t][q] = u32x4{0, 0, 0, 0};
+        if (k + 16 * (q >> 1) < a.K)
+          xv[u][t][q] = *reinterpret_cast<const u32x4*>(xp[t] + 128 * c + 8 * q);
+      }
+  };
+  // a wave's chunks are consecutive: two of them share the cache lines of the codes
+  const int first = nc * wave / NW, last = nc * (wave + 1) / NW;
+  if (first < last) {
+    load_w(0, first);
+    if constexpr (kXDepth == 2) load_x(0, first);
+  }
+  for (int c0 = first; c0 < last; c0 += 2) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int c = c0 + u;
+      if (c >= last) break;                             // uniform
+      constexpr bool kAhead = kXDepth == 2;
+      const int v = kAhead ? u : 0;
+      if (c + 1 < last) load_w(u ^ 1, c + 1);
+      if (!kAhead || c + 1 < last) load_x(kAhead ? u ^ 1 : 0, kAhead ? c + 1 : c);
+#pragma unroll
+      for (int r = 0; r < G; ++r) {
+        const float sf[2] = {e4m3_to_f32(s[u][r]), e4m3_to_f32(s[u][r] >> 8)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bf16x8 wq = e2m1_scaled8(w[u][r][q], sf[q >> 1]);
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                wq, __builtin_bit_cast(bf16x8, xv[v][t][q]), acc[r][t], 0, 0, 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < G; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      *reinterpret_cast<f32x4*>(&red[wave][16 * t + l16][16 * r + 4 * g]) = acc[r][t];
+  __syncthreads();
+  const float alpha = a.alpha[0];
+  for (int i = tid; i < kRows * 16 * TT; i += NW * 64) {
+    const int row = i % kRows, t = i / kRows;
+    float v = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NW; ++u) v += red[u][t][row];
+    if (n0 + row < a.N && t0 + t < a.T) {
+      const int64_t o = static_cast<int64_t>(t0 + t) * a.N + n0 + row;
+      if (a.y_f32) a.y_f32[o] = v * alpha;
+      else a.y[o] = f32_to_bf16(v * alpha);
+    }
+  }
+}
+
+template <int RW, int TT, int NW>
+static hipError_t launch_dot(const MatvecArgs& a, hipStream_t stream) {
+  const dim3 grid((a.N + NW * RW - 1) / (NW * RW));
+  const size_t lds = static_cast<size_t>(a.T) * a.K * 2;
+  if (lds <= kDotLdsBytes)
+    matvec_dot_kernel<RW, TT, NW, true><<<grid, dim3(NW * 64), lds, stream>>>(a);
+  else
+    matvec_dot_kernel<RW, TT, NW, false><<<grid, dim3(NW * 64), 0, stream>>>(a);
   return hipGetLastError();
+}
+
+template <int G, int TT, int NW>
+static hipError_t launch_mfma(const MatvecArgs& a, hipStream_t stream) {
+  const dim3 grid((a.N + 16 * G - 1) / (16 * G), (a.T + 16 * TT - 1) / (16 * TT));
+  if (a.K % 32 == 0) matvec_mfma_kernel<G, TT, NW, true><<<grid, dim3(NW * 64), 0, stream>>>(a);
+  else matvec_mfma_kernel<G, TT, NW, false><<<grid, dim3(NW * 64), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+// Rows per workgroup by the number of workgroups that leaves.  One and two tokens: 16 rows,
+// 8 where that would not give every CU a workgroup of 16 (one token, us: N = 896, K = 3584
+// 3.2 with 8 rows, 4.0 with 16, 5.8 with 32; N = 16384, K = 7168 18.7, 16.1, 17.1).  More
+// tokens: 64, 32 or 16 rows, the most that still fill 7/8 of the CUs (16 tokens, us: N = 16384,
+// K = 7168 26.0, 30.7, 42.2; N = 7181 22.0, 15.7, 21.8; N = 896, K = 3584 13.0, 8.7, 6.8).
+// Two tokens stay with the dot products (N = 7168 11.8 us against 12.6).
+hipError_t launch_matvec_nvfp4(const MatvecArgs& a, hipStream_t stream) {
+  if (a.T <= 2) {
+    const bool few = a.N < 8 * a.cus;
+    if (a.T == 1) return few ? launch_dot<1, 1, 8>(a, stream) : launch_dot<2, 1, 8>(a, stream);
+    return few ? launch_dot<1, 2, 8>(a, stream) : launch_dot<2, 2, 8>(a, stream);
+  }
+  const int fill = a.cus * 7 / 8;
+  const bool two = a.N >= 32 * fill;
+  if (a.T <= 16) {
+    if (a.N >= 64 * fill) return launch_mfma<4, 1, 8>(a, stream);
+    return two ? launch_mfma<2, 1, 8>(a, stream) : launch_mfma<1, 1, 8>(a, stream);
+  }
+  if (a.T <= 32) return two ? launch_mfma<2, 2, 8>(a, stream) : launch_mfma<1, 2, 8>(a, stream);
+  return two ? launch_mfma<2, 4, 8>(a, stream) : launch_mfma<1, 4, 8>(a, stream);
 }
 
 }  // namespace rmoe
