@@ -18,155 +18,182 @@ namespace rmoe {
 template <int Q>
 using acc_t = typename AccOf<Q>::type;
 
-// ---------------------------------------------------------------------------------------
-// Tiles of up to 128 rows.  A workgroup of four wavefronts multiplies one tile of an expert's
-// rows with 128 weight rows, 32 per wavefront.  Each weight is used by one wavefront only, so
-// weights go from memory to registers, kDepth chunks of 128 bytes ahead; the token rows are
-// shared, so they pass through LDS in double-buffered stages of CPS chunks.
-// ---------------------------------------------------------------------------------------
-constexpr int kMidRows = 128, kMidWaves = 4, kMidThreads = kMidWaves * 64, kMidWR = 2;
-constexpr int kMidStageBytes = 16384;
+// Sixteen zero bytes: what a lane loads in the place of bytes past the end of K.
+__device__ const u32x4 g_zero16 = {0u, 0u, 0u, 0u};
 
-template <int Q, bool SITU, int MT>
-__device__ __forceinline__ void mid_tile(const GroupedArgs& a, const TileRows& tr, int cb,
-                                         uint8_t* stage) {
-  constexpr int WR = kMidWR, kDepth = 4;
-  constexpr int CPS = MT <= 2 ? 4 : MT <= 4 ? 2 : 1;         // chunks per stage
-  constexpr int kPieces = CPS * 8;                           // 16-byte pieces of a row per stage
-  constexpr int PPT = MT * 16 * kPieces / kMidThreads;       // pieces per thread
-  static_assert(MT * 16 * CPS * 128 <= kMidStageBytes && PPT * kMidThreads == MT * 16 * kPieces, "");
-  constexpr int kCols = kMidWaves * WR * 16 / (SITU ? 2 : 1);
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int g = lane >> 4, l16 = lane & 15;
-  const int KB = a.KB, nc = (KB + 127) / 128;
-  const int c0 = cb * kCols + wave * (kCols / kMidWaves);
-  const uint8_t* wp[WR];
-#pragma unroll
-  for (int r = 0; r < WR; ++r) {
-    const int n = min(c0 + 16 * (SITU ? r >> 1 : r) + l16, a.N - 1);
-    const int64_t row = static_cast<int64_t>(tr.expert) * a.Nw + n + (SITU && (r & 1) ? a.N : 0);
-    wp[r] = a.w + row * KB + 16 * g;
-  }
-  // this thread's pieces of a stage: row q / kPieces, piece q % kPieces, q = tid + 256 i
-  const uint8_t* xp[PPT];
-#pragma unroll
-  for (int i = 0; i < PPT; ++i) {
-    const int row = (tid + kMidThreads * i) / kPieces;
-    // rows that are not there read the first of the tile; the epilogue leaves them out
-    const int64_t src = source_row(a, tr.row0 + (row < tr.nrows ? row : 0));
-    xp[i] = a.x + (src < 0 ? 0 : src) * KB + (tid % kPieces) * 16;
-  }
-  u32x4 xr[PPT], wv[kDepth][WR][2];
-  auto load_x = [&](int s) {
-    const int off = s * (CPS * 128);
-#pragma unroll
-    for (int i = 0; i < PPT; ++i) {
-      xr[i] = u32x4{0, 0, 0, 0};
-      if (off + (tid % kPieces) * 16 < KB)
-        xr[i] = *reinterpret_cast<const u32x4*>(xp[i] + off);
-    }
-  };
-  // LDS stage: [chunk][row][8 pieces], a row's pieces permuted by its low three bits, so that
-  // eight rows' reads of one piece fall on different banks
-  auto store_x = [&](int s) {
-    uint8_t* buf = stage + (s & 1) * kMidStageBytes;
-#pragma unroll
-    for (int i = 0; i < PPT; ++i) {
-      const int q = tid + kMidThreads * i, row = q / kPieces, pc = q % kPieces;
-      *reinterpret_cast<u32x4*>(buf + (pc >> 3) * (MT * 16 * 128) + row * 128 +
-                                (((pc & 7) ^ (row & 7)) << 4)) = xr[i];
-    }
-  };
-  auto load_w = [&](int u, int c) {
-    const int off = 128 * c;
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int r = 0; r < WR; ++r) {
-        if (off + 128 <= KB) {
-          wv[u][r][f] = *reinterpret_cast<const u32x4*>(wp[r] + off + 64 * f);
-        } else {
-          wv[u][r][f] = u32x4{0, 0, 0, 0};
-          if (off + 64 * f + 16 * g < KB)
-            wv[u][r][f] = *reinterpret_cast<const u32x4*>(wp[r] + off + 64 * f);
-        }
-      }
-  };
-  acc_t<Q> acc[WR][MT];
-#pragma unroll
-  for (int r = 0; r < WR; ++r)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[r][m] = acc_t<Q>{0, 0, 0, 0};
-  load_x(0);
-#pragma unroll
-  for (int u = 0; u < kDepth - 1; ++u)
-    if (u < nc) load_w(u, u);
-  store_x(0);
-  __syncthreads();
-  for (int cg = 0; cg < nc; cg += kDepth) {
-#pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      const int c = cg + u;
-      if (c < nc) {
-        const int s = c / CPS;
-        if (u % CPS == 0) load_x(s + 1);
-        if (c + kDepth - 1 < nc) load_w((u + kDepth - 1) % kDepth, c + kDepth - 1);
-        const uint8_t* buf = stage + (s & 1) * kMidStageBytes + (u % CPS) * (MT * 16 * 128) + l16 * 128;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          u32x4 xv[2];
-#pragma unroll
-          for (int f = 0; f < 2; ++f)
-            xv[f] = *reinterpret_cast<const u32x4*>(buf + m * 2048 + (((4 * f + g) ^ (l16 & 7)) << 4));
-#pragma unroll
-          for (int r = 0; r < WR; ++r)
-            acc[r][m] = mma_chunk<Q>(wv[u][r][0], wv[u][r][1], xv[0], xv[1], acc[r][m]);
-        }
-        if (u % CPS == CPS - 1 || c == nc - 1) {
-          store_x(s + 1);
-          __syncthreads();
-        }
-      }
-    }
-  }
-  constexpr int C = SITU ? WR / 2 : WR;
-  Epilogue<Q, SITU, C, MT> out(a);
-  out.begin(tr.expert, [&](int c) { return c0 + 16 * c + 4 * g; },
-            [&](int m) { return 16 * m + l16 < tr.nrows ? tr.row0 + 16 * m + l16 : -1; });
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (out.row[m] < 0) continue;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      out.store(c, m, out.columns(c, m, acc[SITU ? 2 * c : c][m], acc[SITU ? 2 * c + 1 : c][m]));
-  }
+typedef const __attribute__((address_space(1))) void* global_ptr;
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// The wave's 64 x 16 bytes from each lane's address into consecutive LDS bytes.
+__device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)dst, 16, 0, 0);
 }
 
-template <int Q, bool SITU>
-__global__ __launch_bounds__(kMidThreads, 2) void grouped_mid_kernel(GroupedArgs a) {
+// The s_waitcnt operand for at most vm vector memory operations under way and no LDS one.
+constexpr int wait_vm_lds(int vm) { return (vm & 15) | 0x70 | (vm >> 4) << 14; }
+
+// ---------------------------------------------------------------------------------------
+// Tiles of up to BM rows (32, 64 or 128).  A workgroup of NW wavefronts multiplies one tile of
+// an expert's rows with 32 NW weight rows, 32 per wavefront.  Both operands go from memory
+// straight into LDS in chunks of 128 bytes of K, in a ring of three chunks that runs on over
+// the border between two items.  Every wavefront issues the same number of loads per chunk, so
+// one counted wait per chunk is enough: a chunk is there when no more loads are under way than
+// were issued after it.
+// ---------------------------------------------------------------------------------------
+constexpr int kRing = 3;
+
+template <int Q, bool SITU, int BM, int NW, int PER_CU>
+__global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(GroupedArgs a) {
+  constexpr int kRows = 32 * NW, kCols = kRows / (SITU ? 2 : 1);
+  constexpr int kXLoads = BM / (8 * NW), kLoads = 4 + kXLoads;       // per wavefront and chunk
+  static_assert(kXLoads * 8 * NW == BM, "");
   extern __shared__ int32_t s_tile[];
-  __shared__ alignas(16) uint8_t stage[2 * kMidStageBytes];
-  scan_experts<kMidWaves>(a, s_tile, [](int n) { return (n + kMidRows - 1) / kMidRows; });
-  constexpr int kCols = kMidWaves * kMidWR * 16 / (SITU ? 2 : 1);
+  __shared__ alignas(16) uint8_t s_w0[kRows * 128], s_w1[kRows * 128], s_w2[kRows * 128];
+  __shared__ alignas(16) uint8_t s_x0[BM * 128], s_x1[BM * 128], s_x2[BM * 128];
+  scan_experts<NW>(a, s_tile, [](int n) { return (n + BM - 1) / BM; });
   const int nblk = (a.N + kCols - 1) / kCols;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int g = lane >> 4, l16 = lane & 15;
+  const int KB = a.KB;
+  // an item takes whole rounds of the ring (chunks past the end of K are zeros), so that every
+  // item starts with the first buffers
+  const int nc = (KB + 128 * kRing - 1) / (128 * kRing) * kRing;
+  const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
   ItemWalk walk(a, s_tile, nblk);
-  TileRows tr;
-  int cb;
-  while (walk.next<kMidRows>(&tr, &cb)) {
+  TileRows ld;
+  int ld_cb = 0;
+  bool more = walk.next<BM>(&ld, &ld_cb);
+  if (!more) return;                                   // the whole workgroup
+
+  // Load j of a wavefront fills rows 8 j + lane / 8 of its 32 weight rows, or of its token
+  // rows; slot lane % 8 of a row holds piece (lane % 8) ^ (row % 8), so that eight rows' reads
+  // of one piece fall on different banks.
+  const uint8_t *wp[4], *xp[kXLoads];
+  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;
+  auto begin_item = [&]() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // LDS row 16 r + m holds MFMA row m of group r: columns 8 (m / 4) + 4 r + m % 4 of the
+      // wavefront's 32, so that a lane's two groups make eight consecutive columns; with SiTU
+      // column m, the gate row in group 0 and the up row in group 1
+      const int l8 = lane >> 3, r = j >> 1, m = 8 * (j & 1) + l8;
+      const int n = ld_cb * kCols + wave * (kCols / NW) + (SITU ? m : 8 * (m >> 2) + 4 * r + (m & 3));
+      const int64_t row = static_cast<int64_t>(ld.expert) * a.Nw + min(n, a.N - 1) + (SITU && r ? a.N : 0);
+      wp[j] = a.w + row * KB + piece;
+    }
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j) {
+      const int row = 8 * (NW * j + wave) + (lane >> 3);
+      // rows that are not there read the first of the tile; the epilogue leaves them out
+      const int64_t src = source_row(a, ld.row0 + (row < ld.nrows ? row : 0));
+      xp[j] = a.x + (src < 0 ? 0 : src) * KB + piece;
+    }
+  };
+  auto load = [&](uint8_t* sw, uint8_t* sx, int c) {
+    const int off = 128 * c;
+    const bool in = off + piece < KB;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      load_to_lds(in ? wp[j] + off : zero, sw + (32 * wave + 8 * j) * 128);
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j)
+      load_to_lds(in ? xp[j] + off : zero, sx + 8 * (NW * j + wave) * 128);
+  };
+
+  auto item = [&](auto mt_c, const TileRows tr, const int cb) {
+    constexpr int MT = decltype(mt_c)::value;
+    acc_t<Q> acc[2][MT];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[r][m] = acc_t<Q>{0, 0, 0, 0};
+    // this wavefront's loads of the chunk are in LDS, and it is done reading the buffers that
+    // the next loads write; after the barrier that holds for the workgroup
+    auto arrive = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(wait_vm_lds((kRing - 2) * kLoads));
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto compute = [&](const uint8_t* sw, const uint8_t* sx) {
+      u32x4 wf[2][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          wf[r][f] = *reinterpret_cast<const u32x4*>(sw + (32 * wave + 16 * r + l16) * 128 +
+                                                     (((4 * f + g) ^ (l16 & 7)) << 4));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        u32x4 xf[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          xf[f] = *reinterpret_cast<const u32x4*>(sx + (16 * m + l16) * 128 +
+                                                  (((4 * f + g) ^ (l16 & 7)) << 4));
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          acc[r][m] = mma_chunk<Q>(wf[r][0], wf[r][1], xf[0], xf[1], acc[r][m]);
+      }
+    };
+    for (int c = 0; c < nc; c += kRing) {
+      const bool last = c + kRing == nc;
+      arrive();
+      load(s_w2, s_x2, c + 2);
+      compute(s_w0, s_x0);
+      arrive();
+      // after an item's last chunk the first of the next item, or of this one again behind the
+      // last item, so that the number of loads under way stays the same
+      if (last) {
+        more = walk.next<BM>(&ld, &ld_cb);
+        if (more) begin_item();
+      }
+      load(s_w0, s_x0, last ? 0 : c + 3);
+      compute(s_w1, s_x1);
+      arrive();
+      load(s_w1, s_x1, last ? 1 : c + 4);
+      compute(s_w2, s_x2);
+    }
+    constexpr int C = SITU ? 1 : 2;
+    Epilogue<Q, SITU, C, MT> out(a);
+    out.begin(tr.expert,
+              [&](int n) { return cb * kCols + wave * (kCols / NW) + (SITU ? 4 * g : 8 * g + 4 * n); },
+              [&](int m) { return 16 * m + l16 < tr.nrows ? tr.row0 + 16 * m + l16 : -1; });
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (out.row[m] < 0) continue;
+      if constexpr (SITU)
+        out.store(0, m, out.columns(0, m, acc[0][m], acc[1][m]));
+      else
+        out.store(0, m, out.columns(0, m, acc[0][m], acc[0][m]),
+                  out.columns(1, m, acc[1][m], acc[1][m]));
+    }
+  };
+
+  begin_item();
+  TileRows tr = ld;
+  int cb = ld_cb;
+  // The load side is two chunks ahead: it is in the item that the other side begins.
+  load(s_w0, s_x0, 0);
+  load(s_w1, s_x1, 1);
+  for (;;) {
     const int mt = (tr.nrows + 15) / 16;
-    if (mt <= 1) mid_tile<Q, SITU, 1>(a, tr, cb, stage);
-    else if (mt <= 2) mid_tile<Q, SITU, 2>(a, tr, cb, stage);
-    else if (mt <= 4) mid_tile<Q, SITU, 4>(a, tr, cb, stage);
-    else if (mt <= 6) mid_tile<Q, SITU, 6>(a, tr, cb, stage);
-    else mid_tile<Q, SITU, 8>(a, tr, cb, stage);
+    if (mt <= 1) item(IntC<1>{}, tr, cb);
+    else if (mt <= 2) item(IntC<2>{}, tr, cb);
+    else if (BM == 64 || mt <= 4) item(IntC<BM >= 64 ? 4 : 2>{}, tr, cb);
+    else if (mt <= 6) item(IntC<BM >= 128 ? 6 : 2>{}, tr, cb);
+    else item(IntC<BM >= 128 ? 8 : 2>{}, tr, cb);
+    if (!more) break;
+    tr = ld;
+    cb = ld_cb;
   }
+  __builtin_amdgcn_s_waitcnt(0);                       // no load into LDS outlives the workgroup
 }
 
-template <int Q, bool SITU>
+template <int Q, bool SITU, int BM, int NW, int PER_CU>
 static hipError_t launch_mid(const GroupedArgs& a, hipStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(a.cus / a.xcds * a.xcds * 2);
-  grouped_mid_kernel<Q, SITU><<<dim3(grid), dim3(kMidThreads), (static_cast<size_t>(a.E) + 1) * 4,
-                                stream>>>(a);
+  const unsigned grid = static_cast<unsigned>(a.cus / a.xcds * a.xcds * PER_CU);
+  grouped_mid_kernel<Q, SITU, BM, NW, PER_CU>
+      <<<dim3(grid), dim3(NW * 64), (static_cast<size_t>(a.E) + 1) * 4, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -178,17 +205,6 @@ static hipError_t launch_mid(const GroupedArgs& a, hipStream_t stream) {
 // ---------------------------------------------------------------------------------------
 constexpr int kBigTile = 256, kBigWaves = 8, kBigThreads = kBigWaves * 64;
 constexpr int kBigOperandBytes = kBigTile * 128;
-
-// Sixteen zero bytes: what a lane loads in the place of rows and columns that are not there.
-__device__ const u32x4 g_zero16 = {0u, 0u, 0u, 0u};
-
-typedef const __attribute__((address_space(1))) void* global_ptr;
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
-// The wave's 64 x 16 bytes from each lane's address into consecutive LDS bytes.
-__device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* dst) {
-  __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)dst, 16, 0, 0);
-}
 
 template <int Q, bool SITU>
 __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs a) {
@@ -363,7 +379,10 @@ static hipError_t launch_big(const GroupedArgs& a, hipStream_t stream) {
 template <int Q, bool SITU>
 static hipError_t launch_one(const GroupedArgs& a, hipStream_t stream) {
   if (a.E <= 1024 && a.R >= a.E * 256) return launch_big<Q, SITU>(a, stream);
-  return launch_mid<Q, SITU>(a, stream);
+  if (a.R <= 12 * static_cast<int64_t>(a.E)) return launch_mid<Q, SITU, 32, 4, 2>(a, stream);
+  if (a.R <= 40 * static_cast<int64_t>(a.E) || a.E > 2048)
+    return launch_mid<Q, SITU, 64, 4, 2>(a, stream);
+  return launch_mid<Q, SITU, 128, 8, 1>(a, stream);
 }
 
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream) {
