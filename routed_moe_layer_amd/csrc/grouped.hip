@@ -9,6 +9,8 @@
 // bytes = two fragments: two 16x16x32 BF16 or 16x16x64 int8 products, or one 16x16x128
 // E4M3 product.  Weights are the A operand and token rows the B operand, so a lane ends up
 // with four consecutive output columns of one token row.
+#include <algorithm>
+
 #include "common.h"
 #include "grouped.h"
 #include "kernels.h"
@@ -29,27 +31,48 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)dst, 16, 0, 0);
 }
 
+// A buffer of a ring beyond its first three.
+template <int U, int BYTES>
+__device__ __forceinline__ uint8_t* more_ring() {
+  __shared__ alignas(16) uint8_t s_more[BYTES];
+  return s_more;
+}
+
+// f(IntC<0>), ..., f(IntC<S - 1>).
+template <int S, int U = 0, class F>
+__device__ __forceinline__ void for_ring(F f) {
+  f(IntC<U>{});
+  if constexpr (U + 1 < S) for_ring<S, U + 1>(f);
+}
+
 // The s_waitcnt operand for at most vm vector memory operations under way and no LDS one.
 constexpr int wait_vm_lds(int vm) { return (vm & 15) | 0x70 | (vm >> 4) << 14; }
 
 // ---------------------------------------------------------------------------------------
 // Tiles of up to BM rows (32, 64 or 128).  A workgroup of NW wavefronts multiplies one tile of
 // an expert's rows with 32 NW weight rows, 32 per wavefront.  Both operands go from memory
-// straight into LDS in chunks of 128 bytes of K, in a ring of three chunks that runs on over
-// the border between two items.  Every wavefront issues the same number of loads per chunk, so
+// straight into LDS in chunks of 128 bytes of K, in a ring of S chunks that runs on over the
+// border between two items.  Every wavefront issues the same number of loads per chunk, so
 // one counted wait per chunk is enough: a chunk is there when no more loads are under way than
 // were issued after it.
 // ---------------------------------------------------------------------------------------
-constexpr int kRing = 3;
-
-template <int Q, bool SITU, int BM, int NW, int PER_CU>
+template <int Q, bool SITU, int BM, int NW, int PER_CU, int S>
 __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(GroupedArgs a) {
   constexpr int kRows = 32 * NW, kCols = kRows / (SITU ? 2 : 1);
   constexpr int kXLoads = BM / (8 * NW), kLoads = 4 + kXLoads;       // per wavefront and chunk
   static_assert(kXLoads * 8 * NW == BM, "");
   extern __shared__ int32_t s_tile[];
-  __shared__ alignas(16) uint8_t s_w0[kRows * 128], s_w1[kRows * 128], s_w2[kRows * 128];
-  __shared__ alignas(16) uint8_t s_x0[BM * 128], s_x1[BM * 128], s_x2[BM * 128];
+  // the ring's buffers: arrays of their own, so that the compiler sees which loads into LDS a
+  // read has to wait for (none, after the counted wait); weights, then token rows
+  __shared__ alignas(16) uint8_t s_0[(kRows + BM) * 128], s_1[(kRows + BM) * 128],
+      s_2[(kRows + BM) * 128];
+  auto ring = [&](auto u) {
+    constexpr int U = decltype(u)::value % S;
+    if constexpr (U == 0) return &s_0[0];
+    else if constexpr (U == 1) return &s_1[0];
+    else if constexpr (U == 2) return &s_2[0];
+    else return more_ring<U, (kRows + BM) * 128>();
+  };
   scan_experts<NW>(a, s_tile, [](int n) { return (n + BM - 1) / BM; });
   const int nblk = (a.N + kCols - 1) / kCols;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -57,7 +80,7 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
   const int KB = a.KB;
   // an item takes whole rounds of the ring (chunks past the end of K are zeros), so that every
   // item starts with the first buffers
-  const int nc = (KB + 128 * kRing - 1) / (128 * kRing) * kRing;
+  const int nc = (KB + 128 * S - 1) / (128 * S) * S;
   const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
   ItemWalk walk(a, s_tile, nblk);
   TileRows ld;
@@ -89,12 +112,13 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
       xp[j] = a.x + (src < 0 ? 0 : src) * KB + piece;
     }
   };
-  auto load = [&](uint8_t* sw, uint8_t* sx, int c) {
+  auto load = [&](uint8_t* buf, int c) {
+    uint8_t* sx = buf + kRows * 128;
     const int off = 128 * c;
     const bool in = off + piece < KB;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      load_to_lds(in ? wp[j] + off : zero, sw + (32 * wave + 8 * j) * 128);
+      load_to_lds(in ? wp[j] + off : zero, buf + (32 * wave + 8 * j) * 128);
 #pragma unroll
     for (int j = 0; j < kXLoads; ++j)
       load_to_lds(in ? xp[j] + off : zero, sx + 8 * (NW * j + wave) * 128);
@@ -111,11 +135,12 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
     // the next loads write; after the barrier that holds for the workgroup
     auto arrive = [&]() {
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(wait_vm_lds((kRing - 2) * kLoads));
+      __builtin_amdgcn_s_waitcnt(wait_vm_lds((S - 2) * kLoads));
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
     };
-    auto compute = [&](const uint8_t* sw, const uint8_t* sx) {
+    auto compute = [&](const uint8_t* sw) {
+      const uint8_t* sx = sw + kRows * 128;
       u32x4 wf[2][2];
 #pragma unroll
       for (int r = 0; r < 2; ++r)
@@ -135,23 +160,22 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
           acc[r][m] = mma_chunk<Q>(wf[r][0], wf[r][1], xf[0], xf[1], acc[r][m]);
       }
     };
-    for (int c = 0; c < nc; c += kRing) {
-      const bool last = c + kRing == nc;
-      arrive();
-      load(s_w2, s_x2, c + 2);
-      compute(s_w0, s_x0);
-      arrive();
-      // after an item's last chunk the first of the next item, or of this one again behind the
-      // last item, so that the number of loads under way stays the same
-      if (last) {
-        more = walk.next<BM>(&ld, &ld_cb);
-        if (more) begin_item();
-      }
-      load(s_w0, s_x0, last ? 0 : c + 3);
-      compute(s_w1, s_x1);
-      arrive();
-      load(s_w1, s_x1, last ? 1 : c + 4);
-      compute(s_w2, s_x2);
+    for (int c = 0; c < nc; c += S) {
+      const bool last = c + S == nc;
+      for_ring<S>([&](auto u) {
+        constexpr int U = decltype(u)::value;
+        arrive();
+        // after an item's last chunk the first of the next item, or of this one again behind
+        // the last item, so that the number of loads under way stays the same
+        if constexpr (U == 1) {
+          if (last) {
+            more = walk.next<BM>(&ld, &ld_cb);
+            if (more) begin_item();
+          }
+        }
+        load(ring(IntC<U + S - 1>{}), U > 0 && last ? U - 1 : c + U + S - 1);
+        compute(ring(u));
+      });
     }
     constexpr int C = SITU ? 1 : 2;
     Epilogue<Q, SITU, C, MT> out(a);
@@ -172,9 +196,8 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
   begin_item();
   TileRows tr = ld;
   int cb = ld_cb;
-  // The load side is two chunks ahead: it is in the item that the other side begins.
-  load(s_w0, s_x0, 0);
-  load(s_w1, s_x1, 1);
+  // The load side is S - 1 chunks ahead: it is in the item that the other side begins.
+  for_ring<S - 1>([&](auto u) { load(ring(u), decltype(u)::value); });
   for (;;) {
     const int mt = (tr.nrows + 15) / 16;
     if (mt <= 1) item(IntC<1>{}, tr, cb);
@@ -189,10 +212,10 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
   __builtin_amdgcn_s_waitcnt(0);                       // no load into LDS outlives the workgroup
 }
 
-template <int Q, bool SITU, int BM, int NW, int PER_CU>
+template <int Q, bool SITU, int BM, int NW, int PER_CU, int S>
 static hipError_t launch_mid(const GroupedArgs& a, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(a.cus / a.xcds * a.xcds * PER_CU);
-  grouped_mid_kernel<Q, SITU, BM, NW, PER_CU>
+  grouped_mid_kernel<Q, SITU, BM, NW, PER_CU, S>
       <<<dim3(grid), dim3(NW * 64), (static_cast<size_t>(a.E) + 1) * 4, stream>>>(a);
   return hipGetLastError();
 }
@@ -376,13 +399,33 @@ static hipError_t launch_big(const GroupedArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Which kernel.  Larger tiles read the weights for more rows at once; smaller ones and smaller
+// blocks of weight rows make more work items.  items() is an upper bound of the items of a
+// kernel (the host does not know the rows of each expert), `few` three quarters of the CUs.
+// Measured on one MI355X, BF16 unless said otherwise, us with tiles of 256 / 128 / 64 / 32 rows:
+//   many rows per expert: 64 experts x 512 rows, N = 768, K = 3584  238 / 242 / 299 / -, but
+//     x 256 rows (half of the experts above one tile) 208 / 130 / 174 / -;
+//   the same with too few items: one expert, 512 rows, N = K = 7168  151 / 89 / 69 / 112;
+//   few rows, many items: FC2 of 1024 Zipf tokens over 896 experts, N = 3584, K = 384
+//     - / 482 / 505 / 602;
+//   few rows, few items: 8 experts x 32 rows, N = K = 4096  - / 54 / 46 / 60;
+//     one expert, 64 rows, N = K = 7168  - / 59 / 41 / 26; one token's 16 experts, N = 384 with
+//     SiTU, K = 3584  37 with blocks of 128 weight rows and 3 chunks, 22 with 64 and 6, whose
+//     longer ring loses on short K (FC2 of 16 tokens over 896 experts, K = 384: 115 and 139).
 template <int Q, bool SITU>
 static hipError_t launch_one(const GroupedArgs& a, hipStream_t stream) {
-  if (a.E <= 1024 && a.R >= a.E * 256) return launch_big<Q, SITU>(a, stream);
-  if (a.R <= 12 * static_cast<int64_t>(a.E)) return launch_mid<Q, SITU, 32, 4, 2>(a, stream);
-  if (a.R <= 40 * static_cast<int64_t>(a.E) || a.E > 2048)
-    return launch_mid<Q, SITU, 64, 4, 2>(a, stream);
-  return launch_mid<Q, SITU, 128, 8, 1>(a, stream);
+  const int64_t R = a.R, E = a.E, few = a.cus * 3 / 4;
+  auto items = [&](int tile, int block) {
+    return (std::min(R, E) + R / tile) * ((a.Nw + block - 1) / block);
+  };
+  // (the LDS of the two largest tiles leaves room for so many experts' prefix sums)
+  if (E <= 1024 && R >= 448 * E && items(256, 256) >= few) return launch_big<Q, SITU>(a, stream);
+  const int64_t items128 = items(128, 256);
+  if (E <= 2048 && (items128 >= 8 * a.cus || (R > 40 * E && items128 >= few)))
+    return launch_mid<Q, SITU, 128, 8, 1, 3>(a, stream);
+  if (R > 24 * E && items(64, 128) >= few) return launch_mid<Q, SITU, 64, 4, 2, 3>(a, stream);
+  if (a.KB >= 2048) return launch_mid<Q, SITU, 32, 2, 2, 6>(a, stream);
+  return launch_mid<Q, SITU, 32, 4, 2, 3>(a, stream);
 }
 
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream) {

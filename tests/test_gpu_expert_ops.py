@@ -285,6 +285,10 @@ GROUPED = [
     (65, 2, 64, 256, "one"), (200, 900, 40, 144, "uniform"), (333, 7, 257, 528, "zipf"),
     (1000, 9, 128, 512, "one"), (2500, 20, 384, 1024, "zipf"), (700, 3, 1000, 272, "uniform"),
     (3000, 2, 256, 2048, "uniform"), (129, 1, 36, 3600, "one"), (50, 10240, 16, 32, "uniform"),
+    # every tile size, with items enough and too few, ragged N and K and odd chunk counts
+    (33, 1, 1100, 2064, "one"), (600, 1, 5000, 272, "one"), (20000, 3, 1031, 400, "zipf"),
+    (9000, 16, 3000, 144, "zipf"), (5000, 600, 2051, 144, "zipf"), (70000, 2500, 24, 64, "uniform"),
+    (300000, 5000, 40, 32, "zipf"), (31000, 65, 96, 48, "uniform"), (1000, 1, 20000, 1040, "one"),
 ]
 
 
