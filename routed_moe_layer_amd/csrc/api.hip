@@ -905,7 +905,10 @@ moe_status_t moe_combine(int32_t T, int32_t H, int32_t k, int32_t R, const uint1
   if (!aligned(rows, 16) || !aligned(expanded_row_idx, 4) || !aligned(route_weights, 2) ||
       !aligned(add, 16) || !aligned(out, 16))
     return MOE_ERR_INVALID_ARG;
-  const CombineArgs a{T, R, H, k, rows, expanded_row_idx, route_weights, add, out};
+  DeviceShape shape;
+  const moe_status_t st = device_shape(&shape);
+  if (st != MOE_OK) return st;
+  const CombineArgs a{T, R, H, k, rows, expanded_row_idx, route_weights, add, out, shape.cus};
   return hip_status(launch_combine(a, reinterpret_cast<hipStream_t>(stream)));
 }
 

@@ -229,6 +229,7 @@ struct CombineArgs {
   const uint16_t* weights;     // [T, k] BF16
   const uint16_t* add;         // [T, H] or null
   uint16_t* out;               // [T, H]
+  int cus;
 };
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
 
