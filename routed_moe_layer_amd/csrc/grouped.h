@@ -161,10 +161,10 @@ struct ItemWalk {
   }
 };
 
-// The same for tiles of BM rows that all cost the same, and one smaller tile per expert for
-// the rest of its rows: the full tiles are dealt first, in equal contiguous parts to the XCDs
-// and one by one to an XCD's workgroups, then the smaller ones, starting with the workgroups
-// that got fewer of the full ones.
+// The same for tiles of BM rows that all cost the same, and up to two smaller ones (of up to
+// half as many rows) per expert for the rest of its rows: the full tiles are dealt first, in
+// equal contiguous parts to the XCDs and one by one to an XCD's workgroups, then the smaller
+// ones, starting with the workgroups that got fewer of the full ones.
 template <int BM>
 struct FullFirstWalk {
   const GroupedArgs& a;
@@ -203,9 +203,9 @@ struct FullFirstWalk {
     *cb = rem / in_run;
     const int e = tile_expert(s, a.E, tile);
     const int2 r = expert_rows(a, e);
-    const int full = (r.y - r.x) / BM;
-    *tr = part ? TileRows{e, r.x + full * BM, r.y - r.x - full * BM}
-               : TileRows{e, r.x + (tile - s[e]) * BM, BM};
+    const int row0 = part ? r.x + (r.y - r.x) / BM * BM + (tile - s[e]) * (BM / 2)
+                          : r.x + (tile - s[e]) * BM;
+    *tr = TileRows{e, row0, min(part ? BM / 2 : BM, r.y - row0)};
     return true;
   }
 };

@@ -235,7 +235,9 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs
   __shared__ alignas(16) uint8_t s_w0[kBigOperandBytes], s_x0[kBigOperandBytes];
   __shared__ alignas(16) uint8_t s_w1[kBigOperandBytes], s_x1[kBigOperandBytes];
   scan_experts<kBigWaves>(a, s_tile, [](int n) { return n / kBigTile; });
-  scan_experts<kBigWaves>(a, s_tile + a.E + 1, [](int n) { return n % kBigTile != 0 ? 1 : 0; });
+  scan_experts<kBigWaves>(a, s_tile + a.E + 1, [](int n) {
+    return (n % kBigTile + kBigTile / 2 - 1) / (kBigTile / 2);
+  });
   constexpr int kCols = kBigTile / (SITU ? 2 : 1);
   const int nblk = (a.N + kCols - 1) / kCols;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
