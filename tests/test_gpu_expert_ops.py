@@ -394,9 +394,93 @@ def test_grouped_gemm_weights_past_32_bit_offsets():
     assert not bool(out[:5].any())
 
 
+# one problem for each tile size and ring that the launch rule chooses between
+KERNELS = [("int8", 40, 1, 1100, 2064), ("bf16", 40, 4, 300, 272), ("e4m3", 600, 1, 5000, 272),
+           ("bf16", 9000, 16, 3000, 144), ("int8", 20000, 3, 2000, 400),
+           ("e4m3", 20000, 3, 2000, 1040)]
+
+
+@pytest.mark.parametrize("q,R,E,N,K", KERNELS)
+def test_grouped_gemm_in_a_graph_repeats_bit_for_bit(q, R, E, N, K):
+    _say(f"grouped graph {q} R={R} E={E} N={N} K={K}")
+    p = _grouped_problem(R, E, N, K, q, False, True, "zipf", seed=12)
+    out, guard = _guarded(R, N)
+    _call(p, out)
+    _check_grouped(p, out)
+    want = out.clone()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        _call(p, out, stream=side)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        out.zero_()
+        _call(p, out)
+        assert torch.equal(out, want)
+    assert _intact(guard)
+
+
+@pytest.mark.parametrize("q,R,E,N,K", KERNELS)
+def test_grouped_gemm_zero_rows_with_the_activation(q, R, E, N, K):
+    _say(f"grouped missing sources {q} R={R}")
+    p = _grouped_problem(R, E, N, K, q, True, True, "uniform", seed=13)
+    gone = [0, R // 2, R - 1]
+    p["row_idx"][gone] = torch.tensor([-1, 3 * p["x_rows"], 2 ** 31 - 1], dtype=torch.int32,
+                                      device="cuda")
+    p["x"].view(torch.uint8)[0] = 0x7F                  # NaN (BF16, E4M3) in the row that stands in
+    out, guard = _guarded(R, N)
+    _call(p, out)
+    torch.cuda.synchronize()
+    assert _intact(guard) and not bool(out[gone].any())
+
+
+def test_grouped_gemm_rows_and_outputs_past_32_bit_offsets():
+    _say("grouped large rows and outputs")
+    R, E, N, K = 300000, 2, 8192, 8192                 # 2.5e9 outputs; x 2.5e9 bytes
+    g = _gen(3)
+    x = torch.zeros((R, K), dtype=torch.int8, device="cuda")
+    last = torch.randint(-127, 128, (300, K), generator=g, device="cuda", dtype=torch.int8)
+    x[R - 300:] = last
+    w = torch.randint(-127, 128, (E, N, K), generator=g, device="cuda", dtype=torch.int8)
+    one = torch.full((R,), 0.01, device="cuda")
+    cum = torch.tensor([R - 150, R], dtype=torch.int32, device="cuda")
+    out = torch.empty((R, N), dtype=BF16, device="cuda")
+    rm.moe_grouped_gemm(R, N, K, E, x, cum, w, out, quant=QUANT["int8"], x_scale=one,
+                        w_scale=torch.full((E, N), 0.02, device="cuda"))
+    assert not bool(out[:R - 300].any())
+    for rows, e in ((slice(0, 150), 0), (slice(150, 300), 1)):
+        want = ref.product(last[rows], w[e])[0] * (0.01 * 0.02)
+        got = out[R - 300:][rows].double()
+        assert bool(((got - want).abs() <= (ref.BF16_HALF_STEP + 2.0 ** -20) * want.abs()).all())
+
+
 # ---------------------------------------------------------------------------------------
 # moe_combine
 # ---------------------------------------------------------------------------------------
+def test_norm_and_combine_past_32_bit_offsets():
+    _say("norm and combine large")
+    T, H = 600000, 4096                                # 2.5e9 values
+    g = _gen(4)
+    x = torch.zeros((T, H), dtype=BF16, device="cuda")
+    x[T - 5:] = _normal(g, 5, H)
+    y = torch.empty_like(x)
+    codes, scales = torch.empty((T, H), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    w = torch.ones(H, dtype=BF16, device="cuda")
+    rm.moe_rmsnorm(T, H, x, None, w, 1e-6, QUANT["int8"], None, y, codes, scales)
+    want = ref.rmsnorm(x[T - 5:], None, w, 1e-6)[1]
+    assert bool(((y[T - 5:].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -16) * want.abs()).all())
+    assert not bool(y[:T - 5].any()) and bool((codes[T - 5:].abs().amax(1) == 127).all())
+    idx = torch.tensor([T - 1, -1, T - 3, 0], dtype=torch.int32, device="cuda")
+    rw = torch.tensor([[0.5, 0.25], [1.0, 2.0]], dtype=BF16, device="cuda")
+    out = torch.empty((2, H), dtype=BF16, device="cuda")
+    rm.moe_combine(2, H, 2, T, x, idx, rw, None, out)
+    want, tol = ref.combine(x, idx, rw, None)
+    assert bool(((out.double() - want).abs() <= tol).all()) and bool(out.any(1).all())
+
+
 def _combine_problem(T, k, H, R, drop, seed=0):
     g = _gen(seed + T + 3 * k + H)
     rows = _normal(g, R, H)
