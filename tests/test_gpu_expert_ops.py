@@ -288,7 +288,7 @@ GROUPED = [
     # every tile size, with items enough and too few, ragged N and K and odd chunk counts
     (33, 1, 1100, 2064, "one"), (600, 1, 5000, 272, "one"), (20000, 3, 1031, 400, "zipf"),
     (9000, 16, 3000, 144, "zipf"), (5000, 600, 2051, 144, "zipf"), (70000, 2500, 24, 64, "uniform"),
-    (300000, 5000, 40, 32, "zipf"), (31000, 65, 96, 48, "uniform"), (1000, 1, 20000, 1040, "one"),
+    (300000, 5000, 40, 32, "zipf"), (60, 10240, 17, 2064, "uniform"), (31000, 65, 96, 48, "uniform"), (1000, 1, 20000, 1040, "one"),
 ]
 
 
