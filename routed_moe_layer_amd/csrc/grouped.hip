@@ -107,9 +107,10 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
       // wavefront's 32, so that a lane's two groups make eight consecutive columns; with SiTU
       // column m, the gate row in group 0 and the up row in group 1
       const int l8 = lane >> 3, r = j >> 1, m = 8 * (j & 1) + l8;
-      const int n = ld_cb * kCols + wave * (kCols / NW) + (SITU ? m : 8 * (m >> 2) + 4 * r + (m & 3));
-      const int64_t row = static_cast<int64_t>(ld.expert) * a.Nw + min(n, a.N - 1) + (SITU && r ? a.N : 0);
-      wp[j] = a.w + row * KB + piece;
+      const int n = ld_cb * kCols + wave * (kCols / NW) +
+                    (SITU ? m : 8 * (m >> 2) + 4 * r + (m & 3));
+      const int64_t row = static_cast<int64_t>(ld.expert) * a.Nw + min(n, a.N - 1);
+      wp[j] = a.w + (row + (SITU && r ? a.N : 0)) * KB + piece;
     }
 #pragma unroll
     for (int j = 0; j < kXLoads; ++j) {
@@ -186,8 +187,8 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
     }
     constexpr int C = SITU ? 1 : 2;
     Epilogue<Q, SITU, C, MT> out(a);
-    out.begin(tr.expert,
-              [&](int n) { return cb * kCols + wave * (kCols / NW) + (SITU ? 4 * g : 8 * g + 4 * n); },
+    const int n0 = cb * kCols + wave * (kCols / NW);
+    out.begin(tr.expert, [&](int n) { return n0 + (SITU ? 4 * g : 8 * g + 4 * n); },
               [&](int m) { return 16 * m + l16 < tr.nrows ? tr.row0 + 16 * m + l16 : -1; });
 #pragma unroll
     for (int m = 0; m < MT; ++m) {

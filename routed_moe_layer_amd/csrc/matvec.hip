@@ -4,8 +4,9 @@
 // Bound by the 9/16 byte per weight, and for the smallest by the latency of a launch: one
 // token x 16384 x 7168 (66 MB) 14.4 us, 4.6 TB/s; the router's logits, one token x 896 x 3584,
 // 3.2 us inside a graph.  With more tokens the token values, which every workgroup reads whole,
-// add to it: 16 tokens x 7181 x 7168 (29 MB) 15.0 us, 10.3 without their loads.  Two kernels: with one or two tokens a wavefront takes
-// whole weight rows, with more the matrix units take 16 tokens at a time.
+// add to it: 16 tokens x 7181 x 7168 (29 MB) 15.0 us, 10.3 without their loads.  Two kernels:
+// with one or two tokens a wavefront takes whole weight rows, with more the matrix units take
+// 16 tokens at a time.
 #include "common.h"
 #include "kernels.h"
 
@@ -17,9 +18,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // One or two tokens.  A wavefront computes RW consecutive weight rows; lane l holds block
 // 64c + l of every row (8 bytes of codes, one scale byte), so a load instruction covers 512
 // contiguous bytes of a row, and the codes of the next kDotDepth steps are on their way while
-// a step is multiplied.  An E2M1 value is exact in BF16: the inner sum is a BF16 dot product accumulated
-// in fp32, multiplied by the block scale in fp32.  The tokens lie in LDS (read once per
-// workgroup; every wavefront reading them from the caches moved as many bytes as the
+// a step is multiplied.  An E2M1 value is exact in BF16: the inner sum is a BF16 dot product
+// accumulated in fp32, multiplied by the block scale in fp32.  The tokens lie in LDS (read once
+// per workgroup; every wavefront reading them from the caches moved as many bytes as the
 // weights), a block's two 16-byte halves in two planes so that the lanes' reads are
 // consecutive.
 // ---------------------------------------------------------------------------------------

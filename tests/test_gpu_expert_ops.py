@@ -175,7 +175,8 @@ def _matvec_check(T, N, K, f32, seed=0):
 @pytest.mark.parametrize("T,N,K", [(1, 1, 16), (1, 896, 3584), (1, 17, 48), (2, 300, 1040),
                                    (3, 64, 2064), (4, 5, 4096), (5, 129, 272), (8, 100, 512),
                                    (16, 333, 3600), (17, 31, 1024), (33, 48, 656), (64, 257, 1008),
-                                   (1, 2051, 65536), (64, 40, 16384)])
+                                   (1, 2051, 65536), (2, 77, 32768), (2, 2100, 512),
+                                   (64, 40, 16384), (12, 14500, 160), (40, 7300, 208)])
 def test_matvec_nvfp4(T, N, K, f32):
     _say(f"matvec T={T} N={N} K={K} f32={f32}")
     _matvec_check(T, N, K, f32)
