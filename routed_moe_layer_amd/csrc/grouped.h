@@ -227,24 +227,32 @@ __device__ __forceinline__ int64_t source_row(const GroupedArgs& a, int i) {
   return s < a.x_rows ? s : -1;
 }
 
-// tanh(v): an odd polynomial for |v| < 1/4 (next Taylor term below 2^-26 of the value),
-// where 1 - exp(-2|v|) would cancel; else (1 - e) / (1 + e), e = exp(-2|v|).
-__device__ __forceinline__ float tanh_f32(float v) {
+// |tanh(v)| as a quotient num / den: an odd polynomial for |v| < 1/4 (next Taylor term below
+// 2^-26 of the value), where 1 - exp(-2|v|) would cancel; else (1 - e) / (1 + e), e = exp(-2|v|).
+__device__ __forceinline__ void tanh_parts(float v, float* num, float* den) {
   const float u = fabsf(v), z = v * v;
   const float e = __builtin_amdgcn_exp2f(-2.8853900817779268f * u);
-  const float far = (1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e);
   float p = __builtin_fmaf(z, 62.0f / 2835.0f, -17.0f / 315.0f);
   p = __builtin_fmaf(z, p, 2.0f / 15.0f);
   p = __builtin_fmaf(z, p, -1.0f / 3.0f);
-  const float near = __builtin_fmaf(u * z, p, u);
-  return copysignf(u < 0.25f ? near : far, v);
+  const bool near = u < 0.25f;
+  *num = near ? __builtin_fmaf(u * z, p, u) : 1.0f - e;
+  *den = near ? 1.0f : 1.0f + e;
 }
 
-// SiTU(g, u) = (beta tanh(g / beta) sigmoid(g)) * (lambda tanh(u / lambda)).
-__device__ __forceinline__ float situ_f32(float g, float u, float beta, float inv_beta, float lam,
-                                          float inv_lam) {
-  const float sig = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
-  return (beta * tanh_f32(g * inv_beta) * sig) * (lam * tanh_f32(u * inv_lam));
+// SiTU(g, u) = (beta tanh(g / beta) sigmoid(g)) * (lambda tanh(u / lambda)), its three
+// quotients over one denominator: three exponentials and one reciprocal, which take four
+// issue slots each, are most of a short product's epilogue.
+__device__ __forceinline__ float situ_f32(float g, float u, float inv_beta, float inv_lam,
+                                          float beta_lam) {
+  const float a = g * inv_beta, b = u * inv_lam;
+  float na, da, nb, db;
+  tanh_parts(a, &na, &da);
+  tanh_parts(b, &nb, &db);
+  const float ds = 1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g);
+  const float mag = beta_lam * na * nb * __builtin_amdgcn_rcpf(da * db * ds);
+  return __uint_as_float(__float_as_uint(mag) ^
+                         ((__float_as_uint(a) ^ __float_as_uint(b)) & 0x80000000u));
 }
 
 // A lane's share of a finished tile: its output columns, in groups of four, of M token rows.
@@ -257,7 +265,7 @@ struct Epilogue {
   int row[M];                            // output row, or -1 (not stored)
   float xs[M];                           // row scale
   bool there[M];                         // the row has a source (zeros are stored otherwise)
-  float beta, lam, ib, il;
+  float ib, il, beta_lam;                // SiTU
 
   __device__ __forceinline__ Epilogue(const GroupedArgs& args) : a(args) {}
   // Everything from memory up front: cols(c) is the first column of group c, rows(m) the
@@ -289,10 +297,10 @@ struct Epilogue {
       }
     }
     if constexpr (SITU) {
-      beta = a.beta ? a.beta[expert] : 4.0f;
-      lam = a.lam ? a.lam[expert] : 25.0f;
+      const float beta = a.beta ? a.beta[expert] : 4.0f, lam = a.lam ? a.lam[expert] : 25.0f;
       ib = 1.0f / beta;
       il = 1.0f / lam;
+      beta_lam = beta * lam;
     }
   }
   // Columns of group c of token m: h the (gate) products, u the up products (SiTU).
@@ -306,7 +314,7 @@ struct Epilogue {
       if constexpr (SITU) {
         float uv = static_cast<float>(u[i]);
         if constexpr (Q != 0) uv = uv * xs[m] * us[c][i];
-        v[i] = situ_f32(v[i], uv, beta, ib, lam, il);
+        v[i] = situ_f32(v[i], uv, ib, il, beta_lam);
       }
       if (!there[m]) v[i] = 0.0f;
     }

@@ -263,7 +263,10 @@ static hipError_t launch_mfma(const MatvecArgs& a, hipStream_t stream) {
 // 3.2 with 8 rows, 4.0 with 16, 5.8 with 32; N = 16384, K = 7168 18.7, 16.1, 17.1).  More
 // tokens: 64, 32 or 16 rows, the most that still fill 7/8 of the CUs (16 tokens, us: N = 16384,
 // K = 7168 26.0, 30.7, 42.2; N = 7181 22.0, 15.7, 21.8; N = 896, K = 3584 13.0, 8.7, 6.8).
-// Two tokens stay with the dot products (N = 7168 11.8 us against 12.6).
+// Two tokens stay with the dot products (N = 7168 11.8 us against 12.6).  More than 16 tokens
+// of a matrix with few rows go 16 at a time, to workgroups of their own that read the same
+// weights, while those are fewer than 7/4 per CU (64 tokens, us: N = 896, K = 3584 7.2 and 16.3
+// together; N = 1650, K = 8720 23.9 and 28.9; N = 3584, K = 3584 21.7 and 17.1).
 hipError_t launch_matvec_nvfp4(const MatvecArgs& a, hipStream_t stream) {
   if (a.T <= 2) {
     const bool few = a.N < 8 * a.cus;
@@ -272,7 +275,8 @@ hipError_t launch_matvec_nvfp4(const MatvecArgs& a, hipStream_t stream) {
   }
   const int fill = a.cus * 7 / 8;
   const bool two = a.N >= 32 * fill;
-  if (a.T <= 16) {
+  const bool apart = ((a.N + 15) / 16) * ((a.T + 15) / 16) < a.cus * 7 / 4;
+  if (a.T <= 16 || apart) {
     if (a.N >= 64 * fill) return launch_mfma<4, 1, 8>(a, stream);
     return two ? launch_mfma<2, 1, 8>(a, stream) : launch_mfma<1, 1, 8>(a, stream);
   }
