@@ -343,8 +343,10 @@ moe_status_t moe_topk_softmax(int32_t T, int32_t num_experts, int32_t top_k,
  *   q MOE_QUANT_E4M3_ROW_DYNAMIC: scales[t] = max_i|y[t, i]| / 448, codes[t, i] =
  *        E4M3(y[t, i] / scales[t]), nearest even;
  * codes are 0 where the scale is 0, and are taken from the fp32 y, not from its BF16
- * rounding.  A row with a NaN or infinite h has a NaN scale.  The squares are summed in
- * fp32: |h| up to 2^60 is what the norm is defined for.
+ * rounding.  A row with a NaN or infinite h (a sum of x and residual past fp32's range is
+ * one) has a NaN scale; so has a row of zeros with eps = 0.  The squares are summed in fp32,
+ * those of a row that leaves its range after a scaling by a power of two: every finite h and
+ * every eps the call takes are within what the norm is defined for.
  * Buffers (device): x, residual (or NULL), residual_out (or NULL; needs residual), y (or
  * NULL) BF16 [T, H]; weight BF16 [H]; codes int8 / E4M3 bytes [T, H] and scales f32 [T]
  * (both NULL with MOE_QUANT_NONE, else both given).  At least one of y and codes is given.

@@ -3,7 +3,9 @@
 //   h = x + res;  y = h * (1 / sqrt(mean(h^2) + eps)) * w;
 //   scale = max|y| / M, code = RN(y / scale) with M = 127 (int8) or 448 (E4M3).
 // h, the mean and y are fp32 throughout: h is rounded to BF16 only where it is stored (the
-// residual stream), y only where it is stored; the codes come from the unrounded y.
+// residual stream), y only where it is stored; the codes come from the unrounded y.  A row
+// whose squares would leave fp32's range is multiplied by a power of two first, which cancels
+// in y.
 //
 // Bound by the bytes: each input is read once and held in registers over the two reductions.
 // 16384 rows of 3584 with the residual, its sum, BF16 and E4M3 rows (529 MB) take 92 us, 5.8
@@ -21,6 +23,19 @@ __device__ __forceinline__ T wave_reduce(T v, F f) {
 }
 
 constexpr int kNormMaxWaves = 16;
+
+// Sums of squares outside [2^-96, 2^100] are taken again of the scaled row.  Below, a square
+// (off by up to 2^-150 where it is subnormal) may have lost bits that count, unless eps of at
+// least 2^-80 hides them; above, the sum of a larger row could be infinite.
+constexpr float kSumLow = 0x1p-96f, kSumHigh = 0x1p100f, kEpsLow = 0x1p-80f;
+// 2^-exponent of the row's largest |h| (bits), 1 for a row of zeros or one that holds an
+// infinity.  At most 2^100: with eps < 2^-80 its square times eps stays finite, and the
+// smallest BF16 values, 2^-133, still have squares of 2^-66.
+__device__ __forceinline__ float row_scale(uint32_t bits) {
+  if (bits == 0u || bits >= 0x7F800000u) return 1.0f;
+  const int e = min(max(127 - static_cast<int>(bits >> 23), -126), 100);
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
 
 // One row per workgroup.  A thread holds C pieces of 8 values: piece p = thread + i * threads.
 // (A row per wavefront with more pieces each was slower: 16384 rows of 3584 108 us, one row
@@ -75,7 +90,34 @@ __global__ __launch_bounds__(kNormMaxWaves * 64) void rmsnorm_kernel(NormArgs a)
   __syncthreads();
   ss = 0.0f;
   for (int i = 0; i < static_cast<int>(blockDim.x >> 6); ++i) ss += s_sum[i];
-  const float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
+  float eps = a.eps;
+  if (ss > kSumHigh || (ss < kSumLow && eps < kEpsLow)) {   // uniform; rare
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(h[i][e]) & 0x7FFFFFFFu);
+    big = wave_reduce(big, [](uint32_t u, uint32_t v) { return max(u, v); });
+    if (lane == 0) s_max[wave] = big;
+    __syncthreads();
+    for (int i = 0; i < static_cast<int>(blockDim.x >> 6); ++i) big = max(big, s_max[i]);
+    const float c = row_scale(big);
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[i][e] *= c;
+        ss = __builtin_fmaf(h[i][e], h[i][e], ss);
+      }
+    eps = eps * c * c;
+    ss = wave_reduce(ss, [](float u, float v) { return u + v; });
+    if (lane == 0) s_sum[wave] = ss;
+    __syncthreads();
+    ss = 0.0f;
+    for (int i = 0; i < static_cast<int>(blockDim.x >> 6); ++i) ss += s_sum[i];
+  }
+  const float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + eps);
   // max|y| as the maximum of the bit patterns: ordered like the values, and a NaN (above
   // every number) stays, so a row that holds one gets a NaN scale instead of losing it.
   uint32_t top = 0;

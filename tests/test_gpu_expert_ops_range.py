@@ -1,0 +1,79 @@
+"""GPU checks of the expert-stage operators at the ends of their types' ranges, against their
+definitions in 64 bits (tests/expert_ops.py)."""
+
+import pytest
+import torch
+
+import routed_moe_layer_amd as rm
+from tests import expert_ops as ref
+from tests.test_gpu_expert_ops import _gen, _norm_check, _normal, _say
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+# ---------------------------------------------------------------------------------------
+# moe_rmsnorm: rows whose squares leave fp32's range
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("q", ["int8", "e4m3"])
+@pytest.mark.parametrize("exp,eps", [(e, v) for e in (-120, -90, -75, -60, -45)
+                                     for v in (0.0, 1e-30, 1e-6)]
+                         + [(e, v) for e in (46, 56, 60, 64, 90, 120) for v in (0.0, 1e-6, 1e30)])
+@pytest.mark.parametrize("T,H", [(3, 72), (2, 3584), (2, 65536)])
+def test_rmsnorm_of_large_and_small_rows(T, H, exp, eps, q):
+    _say(f"rmsnorm T={T} H={H} 2^{exp} eps={eps} {q}")
+    # y is about 2^exp / sqrt(eps), at least 2^-110: its row scales are normal fp32 numbers
+    x = (_normal(_gen(H + exp), T, H, dtype=torch.float32) * 2.0 ** exp).to(BF16)
+    # eps is passed as fp32
+    _norm_check(T, H, q, False, True, x=x, eps=float(torch.tensor(eps)))
+
+
+@pytest.mark.parametrize("value", [2.0 ** 60, 2.0 ** 127, -3.3895e38, 2.0 ** -75, 2.0 ** -126,
+                                   2.0 ** -133])
+def test_rmsnorm_of_rows_of_one_value(value):
+    """With eps = 0 and weight 1 the norm of a constant row is its sign, whatever its value."""
+    for H in (8, 256, 65536):
+        _say(f"rmsnorm constant {value} H={H}")
+        x = torch.full((2, H), value, device="cuda").to(BF16)
+        assert float(x[0, 0]) != 0
+        w, y = torch.ones(H, dtype=BF16, device="cuda"), torch.empty((2, H), dtype=BF16, device="cuda")
+        codes = torch.empty((2, H), dtype=torch.int8, device="cuda")
+        scales = torch.empty(2, device="cuda")
+        rm.moe_rmsnorm(2, H, x, None, w, 0.0, rm.MOE_QUANT_INT8_ROW_DYNAMIC, None, y, codes, scales)
+        sign = 1.0 if value > 0 else -1.0
+        assert bool((y.float() == sign).all()) and bool((codes == int(127 * sign)).all())
+        rel = 2 * ref.norm_rel(H) / 127
+        assert bool(((scales.double() - 1 / 127).abs() <= rel).all())
+
+
+def test_rmsnorm_of_rows_of_very_different_size_in_one_call():
+    """Each row by itself, one of them of zeros, one holding both ends of BF16's range."""
+    _say("rmsnorm mixed rows")
+    H = 1000
+    x = _normal(_gen(3), 6, H, dtype=torch.float32)
+    x *= torch.tensor([2.0 ** 110, 1.0, 2.0 ** -110, 0.0, 2.0 ** 70, 2.0 ** -70], device="cuda")[:, None]
+    x[4, 5], x[4, 6], x[2, 7] = 2.0 ** 127, 2.0 ** -133, 2.0 ** -133
+    x = x.to(BF16)
+    for q in ("int8", "e4m3"):
+        _, y, codes, scales = _norm_check(6, H, q, False, True, x=x, eps=1e-30)
+        assert float(scales[3]) == 0 and not bool(codes[3].any()) and not bool(y[3].any())
+
+
+def test_rmsnorm_of_a_large_row_with_a_residual():
+    """The residual's sum is rounded only where it is stored, at any size; a sum past fp32's
+    range marks its row."""
+    _say("rmsnorm large residual")
+    T, H = 3, 512
+    x, res = (_normal(_gen(i), T, H, std=2.0 ** 100) for i in (4, 5))
+    x[1, 7] = res[1, 7] = 3.3895e38                     # the largest BF16 value
+    w = torch.ones(H, dtype=BF16, device="cuda")
+    h, y = ref.rmsnorm(x, res, w, 0.0)
+    out, res_out = torch.empty_like(x), torch.empty_like(x)
+    codes, scales = torch.empty((T, H), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    rm.moe_rmsnorm(T, H, x, res, w, 0.0, rm.MOE_QUANT_INT8_ROW_DYNAMIC, res_out, out, codes, scales)
+    ok = [0, 2]
+    assert bool(((res_out[ok].double() - h[ok]).abs() <= ref.BF16_HALF_STEP * 1.001 * h[ok].abs()).all())
+    tol = (ref.BF16_HALF_STEP + 2 * ref.norm_rel(H)) * y[ok].abs()
+    assert bool(((out[ok].double() - y[ok]).abs() <= tol).all())
+    assert bool(scales[ok].isfinite().all()) and bool(scales[1].isnan())
