@@ -57,10 +57,14 @@ __device__ __forceinline__ int2 expert_rows(const GroupedArgs& a, int e) {
   return make_int2(lo, hi);
 }
 
-// s[e] = sum of count(rows of expert) over the experts before e, s[E] the total.  Every
-// thread of the workgroup (NW wavefronts) calls this; it ends with a barrier.
+// s[e] = sum of count(rows of expert) over the experts before e, s[E] the total, all cut at
+// `most`, the largest total of rising prefix sums.  (Falling ones give the same rows to several
+// experts: uncut, 10240 experts that claim 2^24 rows in turn make 1.3e9 tiles of 64 rows times
+// the blocks of weight rows, a launch that lasts for minutes.  Tiles past the cut are left out.)
+// Every thread of the workgroup (NW wavefronts) calls this; it ends with a barrier.
 template <int NW, class F>
-__device__ __forceinline__ void scan_experts(const GroupedArgs& a, int32_t* s, F count) {
+__device__ __forceinline__ void scan_experts(const GroupedArgs& a, int32_t* s, int32_t most,
+                                             F count) {
   __shared__ int32_t s_wave[NW];
   constexpr int kThreads = NW * 64;
   const int per = (a.E + kThreads - 1) / kThreads;
@@ -72,6 +76,7 @@ __device__ __forceinline__ void scan_experts(const GroupedArgs& a, int32_t* s, F
     s[e] = n;
     sum += n;
   }
+  sum = min(sum, most);                  // (a cut part alone brings every later sum to the cut)
   int inc = sum;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -85,10 +90,10 @@ __device__ __forceinline__ void scan_experts(const GroupedArgs& a, int32_t* s, F
   for (int i = 0; i < wave; ++i) before += s_wave[i];
   for (int e = lo; e < hi; ++e) {
     const int n = s[e];
-    s[e] = before;
+    s[e] = min(before, most);
     before += n;
   }
-  if (threadIdx.x == kThreads - 1) s[a.E] = before;
+  if (threadIdx.x == kThreads - 1) s[a.E] = min(before, most);
   __syncthreads();
 }
 

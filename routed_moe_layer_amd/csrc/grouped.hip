@@ -80,7 +80,7 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mid_kernel(G
     else if constexpr (U == 2) return &s_2[0];
     else return more_ring<U, (kRows + BM) * 128>();
   };
-  scan_experts<NW>(a, s_tile, [](int n) { return (n + BM - 1) / BM; });
+  scan_experts<NW>(a, s_tile, a.R / BM + min(a.R, a.E), [](int n) { return (n + BM - 1) / BM; });
   const int nblk = (a.N + kCols - 1) / kCols;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g = lane >> 4, l16 = lane & 15;
@@ -248,8 +248,8 @@ __global__ __launch_bounds__(kBigThreads, 2) void grouped_big_kernel(GroupedArgs
   extern __shared__ int32_t s_tile[];                  // two prefix sums of E + 1
   __shared__ alignas(16) uint8_t s_w0[kBigOperandBytes], s_x0[kBigOperandBytes];
   __shared__ alignas(16) uint8_t s_w1[kBigOperandBytes], s_x1[kBigOperandBytes];
-  scan_experts<kBigWaves>(a, s_tile, [](int n) { return n / kBigTile; });
-  scan_experts<kBigWaves>(a, s_tile + a.E + 1, [](int n) {
+  scan_experts<kBigWaves>(a, s_tile, a.R / kBigTile, [](int n) { return n / kBigTile; });
+  scan_experts<kBigWaves>(a, s_tile + a.E + 1, 2 * min(a.R, a.E), [](int n) {
     return (n % kBigTile + kBigTile / 2 - 1) / (kBigTile / 2);
   });
   constexpr int kCols = kBigTile / (SITU ? 2 : 1);

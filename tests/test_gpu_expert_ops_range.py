@@ -6,7 +6,7 @@ import torch
 
 import routed_moe_layer_amd as rm
 from tests import expert_ops as ref
-from tests.test_gpu_expert_ops import _gen, _norm_check, _normal, _say
+from tests.test_gpu_expert_ops import _gen, _guarded, _intact, _norm_check, _normal, _say
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,35 @@ def test_rmsnorm_of_a_large_row_with_a_residual():
     tol = (ref.BF16_HALF_STEP + 2 * ref.norm_rel(H)) * y[ok].abs()
     assert bool(((out[ok].double() - y[ok]).abs() <= tol).all())
     assert bool(scales[ok].isfinite().all()) and bool(scales[1].isnan())
+
+
+# ---------------------------------------------------------------------------------------
+# moe_grouped_gemm: prefix sums that fall
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("R,E,N,K", [
+    (1 << 24, 10240, 16, 16),                           # tiles of 64 rows, 1.3e9 of them uncut
+    (245000, 10240, 16, 16), (245000, 10240, 8, 2048),  # tiles of 32 rows, both ring lengths
+    ((1 << 20) + 77, 2000, 24, 16),                     # tiles of 128 rows
+    (448100, 1000, 40, 16)])                            # tiles of 256 rows
+def test_grouped_gemm_prefix_sums_that_fall(R, E, N, K):
+    """Every other expert claims all rows: the tiles that are worked on stay as many as rising
+    prefix sums could make.  The experts' weights are alike, so that it does not matter which of
+    them a row is multiplied with."""
+    _say(f"grouped falling prefix sums R={R} E={E} N={N} K={K}")
+    g = _gen(R + E)
+    x = torch.randint(-127, 128, (R, K), generator=g, device="cuda", dtype=torch.int8)
+    w1 = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    w = w1.expand(E, N, K).contiguous()
+    cum = torch.zeros(E, dtype=torch.int32, device="cuda")
+    cum[::2] = R
+    out, guard = _guarded(R, N)
+    rm.moe_grouped_gemm(R, N, K, E, x, cum, w, out, quant=rm.MOE_QUANT_INT8_ROW_DYNAMIC,
+                        x_scale=torch.full((R,), 0.5, device="cuda"),
+                        w_scale=torch.full((E, N), 0.25, device="cuda"))
+    torch.cuda.synchronize()
+    assert _intact(guard)
+    # an exact int32 sum below 2^25 times 1/8: one rounding to fp32 and one to BF16
+    for lo in range(0, R, 1 << 20):
+        want = ref.product(x[lo:lo + (1 << 20)], w1)[0] / 8
+        got = out[lo:lo + (1 << 20)].double()
+        assert bool(((got - want).abs() <= (ref.BF16_HALF_STEP + 2.0 ** -20) * want.abs()).all())
