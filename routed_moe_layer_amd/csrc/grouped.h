@@ -247,17 +247,23 @@ __device__ __forceinline__ void tanh_parts(float v, float* num, float* den) {
 
 // SiTU(g, u) = (beta tanh(g / beta) sigmoid(g)) * (lambda tanh(u / lambda)), its three
 // quotients over one denominator: three exponentials and one reciprocal, which take four
-// issue slots each, are most of a short product's epilogue.
-__device__ __forceinline__ float situ_f32(float g, float u, float inv_beta, float inv_lam,
-                                          float beta_lam) {
+// issue slots each, are most of a short product's epilogue.  Beta and lambda each go to their
+// own quotient's numerator: beta * lambda alone may leave fp32's range where SiTU does not
+// (both at 1e20 make it nearly g sigmoid(g) * u).
+__device__ __forceinline__ float situ_f32(float g, float u, float beta, float inv_beta, float lam,
+                                          float inv_lam) {
   const float a = g * inv_beta, b = u * inv_lam;
   float na, da, nb, db;
   tanh_parts(a, &na, &da);
   tanh_parts(b, &nb, &db);
   const float ds = 1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g);
-  const float mag = beta_lam * na * nb * __builtin_amdgcn_rcpf(da * db * ds);
+  const float mag = (beta * na) * (lam * nb) * __builtin_amdgcn_rcpf(da * db * ds);
   return __uint_as_float(__float_as_uint(mag) ^
                          ((__float_as_uint(a) ^ __float_as_uint(b)) & 0x80000000u));
+}
+
+__device__ __forceinline__ float uniform(float v) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
 }
 
 // A lane's share of a finished tile: its output columns, in groups of four, of M token rows.
@@ -270,7 +276,7 @@ struct Epilogue {
   int row[M];                            // output row, or -1 (not stored)
   float xs[M];                           // row scale
   bool there[M];                         // the row has a source (zeros are stored otherwise)
-  float ib, il, beta_lam;                // SiTU
+  float beta, ib, lam, il;               // SiTU
 
   __device__ __forceinline__ Epilogue(const GroupedArgs& args) : a(args) {}
   // Everything from memory up front: cols(c) is the first column of group c, rows(m) the
@@ -302,10 +308,11 @@ struct Epilogue {
       }
     }
     if constexpr (SITU) {
-      const float beta = a.beta ? a.beta[expert] : 4.0f, lam = a.lam ? a.lam[expert] : 25.0f;
-      ib = 1.0f / beta;
-      il = 1.0f / lam;
-      beta_lam = beta * lam;
+      // the same in every lane: kept in scalar registers
+      beta = uniform(a.beta ? a.beta[expert] : 4.0f);
+      lam = uniform(a.lam ? a.lam[expert] : 25.0f);
+      ib = uniform(1.0f / beta);
+      il = uniform(1.0f / lam);
     }
   }
   // Columns of group c of token m: h the (gate) products, u the up products (SiTU).
@@ -319,7 +326,7 @@ struct Epilogue {
       if constexpr (SITU) {
         float uv = static_cast<float>(u[i]);
         if constexpr (Q != 0) uv = uv * xs[m] * us[c][i];
-        v[i] = situ_f32(v[i], uv, ib, il, beta_lam);
+        v[i] = situ_f32(v[i], uv, beta, ib, lam, il);
       }
       if (!there[m]) v[i] = 0.0f;
     }

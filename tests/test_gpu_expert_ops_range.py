@@ -6,7 +6,8 @@ import torch
 
 import routed_moe_layer_amd as rm
 from tests import expert_ops as ref
-from tests.test_gpu_expert_ops import _gen, _guarded, _intact, _norm_check, _normal, _say
+from tests.test_gpu_expert_ops import (KERNELS, _call, _check_grouped, _gen, _grouped_problem,
+                                       _guarded, _intact, _norm_check, _normal, _say)
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +110,19 @@ def test_grouped_gemm_prefix_sums_that_fall(R, E, N, K):
         want = ref.product(x[lo:lo + (1 << 20)], w1)[0] / 8
         got = out[lo:lo + (1 << 20)].double()
         assert bool(((got - want).abs() <= (ref.BF16_HALF_STEP + 2.0 ** -20) * want.abs()).all())
+
+
+# ---------------------------------------------------------------------------------------
+# moe_grouped_gemm: SiTU's parameters
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("beta,lam", [(1e20, 1e20), (1e30, 1e9), (1e-3, 1e30), (1e25, 1e-20)])
+@pytest.mark.parametrize("q,R,E,N,K", KERNELS)
+def test_grouped_gemm_situ_parameters_whose_product_leaves_fp32(q, R, E, N, K, beta, lam):
+    _say(f"grouped SiTU beta={beta} lambda={lam} {q} R={R} E={E} N={N} K={K}")
+    p = _grouped_problem(R, E, N, K, q, True, True, "uniform", seed=21)
+    p["beta"], p["lam"] = torch.full((E,), beta, device="cuda"), torch.full((E,), lam, device="cuda")
+    out, guard = _guarded(R, N)
+    _call(p, out)
+    torch.cuda.synchronize()
+    assert _intact(guard)
+    _check_grouped(p, out)
