@@ -356,18 +356,50 @@ def moe_topk_softmax(T, num_experts, top_k, logits, expert_ids, route_weights, s
         _stream(stream)))
 
 
+# What a buffer of the stages may hold, by the names that _checked's callers use: a text for
+# messages and the names of the tensor types.  BF16 is passed as 16-bit patterns too, and codes
+# and scales of 8 bits or less as bytes.
+_KINDS = {
+    "bf16": ("BF16", "bfloat16 int16 uint16"),
+    "f32": ("float32", "float32"),
+    "i32": ("int32", "int32"),
+    "int8": ("int8", "int8 uint8"),
+    "e4m3": ("E4M3", "float8_e4m3fn uint8"),
+    "nvfp4": ("NVFP4 code bytes", "uint8 int8 float4_e2m1fn_x2"),
+    "e4m3_scale": ("E4M3 scales", "uint8 float8_e4m3fn"),
+    "byte": ("8 bits", "int8 uint8 float8_e4m3fn"),
+}
+_kind_types = {}
+
+
+def _load_types():
+    import torch
+    _kind_types.update({k: frozenset(getattr(torch, n) for n in names.split() if hasattr(torch, n))
+                        for k, (_, names) in _KINDS.items()})
+    return _kind_types
+
+
+def _code_kind(quant):
+    """The kind of 8-bit codes that a quantization makes or takes (the library refuses others)."""
+    if quant == MOE_QUANT_INT8_ROW_DYNAMIC:
+        return "int8"
+    return "e4m3" if quant == MOE_QUANT_E4M3_ROW_DYNAMIC else "byte"
+
+
 def _checked(fn, stream, *buffers):
     """The stream's handle and the addresses of the buffers, which are given as
-    (name, tensor, elements, bytes of one element).
+    (name, tensor, elements, kind), the kind one of _KINDS.
 
-    A tensor is looked at before its address is passed on: on the stream's GPU (the current
-    one unless the stream says otherwise), contiguous, of that element size and at least that
-    many elements; None and int addresses pass as they are."""
-    device, out = None, [None]
-    for name, t, n, size in buffers:
+    A tensor is looked at before its address is passed on: of a type of that kind, on the
+    stream's GPU (the current one unless the stream says otherwise), contiguous and at least
+    that many elements; None and int addresses pass as they are."""
+    types, device, out = _kind_types or _load_types(), None, [None]
+    for name, t, n, kind in buffers:
         if t is None or isinstance(t, int):
             out.append(t)
             continue
+        if t.dtype not in types[kind]:
+            raise ValueError(f"{fn}: {name} holds {t.dtype}, not {_KINDS[kind][0]}")
         at = t.get_device()                    # -1 on the host
         if at != device:
             if at < 0:
@@ -377,9 +409,8 @@ def _checked(fn, stream, *buffers):
             device = at
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} is not contiguous")
-        if t.element_size() != size or t.numel() < n:
-            raise ValueError(f"{fn}: {name} holds {t.numel()} elements of {t.element_size()} bytes, "
-                             f"not {n} of {size}")
+        if t.numel() < n:
+            raise ValueError(f"{fn}: {name} holds {t.numel()} elements, not {n}")
         out.append(t.data_ptr())
     out[0] = _stream_on(fn, stream, device)
     return out
@@ -407,18 +438,19 @@ def _stream_on(fn, stream, device):
 def moe_rmsnorm(T, H, x, residual, weight, eps, quant, residual_out, y, codes, scales,
                 stream=None):
     stream, x, residual, weight, residual_out, y, codes, scales = _checked(
-        "moe_rmsnorm", stream, ("x", x, T * H, 2), ("residual", residual, T * H, 2),
-        ("weight", weight, H, 2), ("residual_out", residual_out, T * H, 2), ("y", y, T * H, 2),
-        ("codes", codes, T * H, 1), ("scales", scales, T, 4))
+        "moe_rmsnorm", stream, ("x", x, T * H, "bf16"), ("residual", residual, T * H, "bf16"),
+        ("weight", weight, H, "bf16"), ("residual_out", residual_out, T * H, "bf16"),
+        ("y", y, T * H, "bf16"), ("codes", codes, T * H, _code_kind(quant)),
+        ("scales", scales, T, "f32"))
     _check("moe_rmsnorm", _lib().moe_rmsnorm(T, H, x, residual, weight, eps, quant, residual_out,
                                              y, codes, scales, stream))
 
 
 def moe_matvec_nvfp4(T, N, K, x, codes, scales, alpha, y, out_f32=False, stream=None):
     stream, x, codes, scales, alpha, y = _checked(
-        "moe_matvec_nvfp4", stream, ("x", x, T * K, 2), ("codes", codes, N * K // 2, 1),
-        ("scales", scales, N * K // 16, 1), ("alpha", alpha, 1, 4),
-        ("y", y, T * N, 4 if out_f32 else 2))
+        "moe_matvec_nvfp4", stream, ("x", x, T * K, "bf16"), ("codes", codes, N * K // 2, "nvfp4"),
+        ("scales", scales, N * K // 16, "e4m3_scale"), ("alpha", alpha, 1, "f32"),
+        ("y", y, T * N, "f32" if out_f32 else "bf16"))
     _check("moe_matvec_nvfp4", _lib().moe_matvec_nvfp4(T, N, K, x, codes, scales, alpha, y,
                                                        int(out_f32), stream))
 
@@ -429,14 +461,14 @@ def moe_grouped_gemm(R, N, K, E, x, expert_cumsum, w, out, quant=MOE_QUANT_NONE,
     """``x_rows`` defaults to R; ``row_div`` counts with ``row_idx`` only."""
     x_rows = R if x_rows is None else x_rows
     row_div = 1 if row_idx is None or row_div is None else row_div
-    size, Nw = 2 if quant == MOE_QUANT_NONE else 1, 2 * N if situ else N
+    kind, Nw = "bf16" if quant == MOE_QUANT_NONE else _code_kind(quant), 2 * N if situ else N
     (stream, x, x_scale, row_idx, expert_cumsum, w, w_scale, situ_beta, situ_linear_beta,
      out) = _checked(
-        "moe_grouped_gemm", stream, ("x", x, x_rows * K, size), ("x_scale", x_scale, x_rows, 4),
-        ("row_idx", row_idx, R, 4), ("expert_cumsum", expert_cumsum, E, 4),
-        ("w", w, E * Nw * K, size), ("w_scale", w_scale, E * Nw, 4),
-        ("situ_beta", situ_beta, E, 4), ("situ_linear_beta", situ_linear_beta, E, 4),
-        ("out", out, R * N, 2))
+        "moe_grouped_gemm", stream, ("x", x, x_rows * K, kind),
+        ("x_scale", x_scale, x_rows, "f32"), ("row_idx", row_idx, R, "i32"),
+        ("expert_cumsum", expert_cumsum, E, "i32"), ("w", w, E * Nw * K, kind),
+        ("w_scale", w_scale, E * Nw, "f32"), ("situ_beta", situ_beta, E, "f32"),
+        ("situ_linear_beta", situ_linear_beta, E, "f32"), ("out", out, R * N, "bf16"))
     _check("moe_grouped_gemm", _lib().moe_grouped_gemm(
         R, N, K, E, quant, MOE_EPILOGUE_SITU if situ else MOE_EPILOGUE_NONE, x, x_scale, x_rows,
         row_idx, row_div, expert_cumsum, w, w_scale, situ_beta, situ_linear_beta, out,
@@ -445,8 +477,9 @@ def moe_grouped_gemm(R, N, K, E, x, expert_cumsum, w, out, quant=MOE_QUANT_NONE,
 
 def moe_combine(T, H, k, R, rows, expanded_row_idx, route_weights, add, out, stream=None):
     stream, rows, expanded_row_idx, route_weights, add, out = _checked(
-        "moe_combine", stream, ("rows", rows, R * H, 2),
-        ("expanded_row_idx", expanded_row_idx, T * k, 4),
-        ("route_weights", route_weights, T * k, 2), ("add", add, T * H, 2), ("out", out, T * H, 2))
+        "moe_combine", stream, ("rows", rows, R * H, "bf16"),
+        ("expanded_row_idx", expanded_row_idx, T * k, "i32"),
+        ("route_weights", route_weights, T * k, "bf16"), ("add", add, T * H, "bf16"),
+        ("out", out, T * H, "bf16"))
     _check("moe_combine", _lib().moe_combine(T, H, k, R, rows, expanded_row_idx, route_weights,
                                              add, out, stream))
