@@ -7,6 +7,8 @@
 // add to it: 16 tokens x 7181 x 7168 (29 MB) 15.0 us, 10.3 without their loads.  Two kernels:
 // with one or two tokens a wavefront takes whole weight rows, with more the matrix units take
 // 16 tokens at a time.
+#include <algorithm>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -258,30 +260,52 @@ static hipError_t launch_mfma(const MatvecArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Rows per workgroup by the number of workgroups that leaves.  One and two tokens: 16 rows,
-// 8 where that would not give every CU a workgroup of 16 (one token, us: N = 896, K = 3584
-// 3.2 with 8 rows, 4.0 with 16, 5.8 with 32; N = 16384, K = 7168 18.7, 16.1, 17.1).  More
-// tokens: 64, 32 or 16 rows, the most that still fill 7/8 of the CUs (16 tokens, us: N = 16384,
-// K = 7168 26.0, 30.7, 42.2; N = 7181 22.0, 15.7, 21.8; N = 896, K = 3584 13.0, 8.7, 6.8).
-// Two tokens stay with the dot products (N = 7168 11.8 us against 12.6).  More than 16 tokens
-// of a matrix with few rows go 16 at a time, to workgroups of their own that read the same
-// weights, while those are fewer than 7/4 per CU (64 tokens, us: N = 896, K = 3584 7.2 and 16.3
-// together; N = 1650, K = 8720 23.9 and 28.9; N = 3584, K = 3584 21.7 and 17.1).
+// One and two tokens: 16 weight rows per workgroup from 24 rows per CU on, 8 below (us with 8
+// and 16 rows, one token: N = 896, K = 3584 3.5 and 4.5; N = 2048 3.8 and 4.7; N = 3584 4.8 and
+// 5.0; N = 5120 5.8 and 6.5; N = 7168 6.7 and 6.7; N = 16384 11.7 and 10.4; two tokens the same
+// way; K = 1792 and 7168 cross between 5120 and 7168 too).  Two tokens stay with the dot
+// products (N = 7168 11.8 us against 12.6).
+//
+// More tokens: 16 G weight rows and 16 TT tokens per workgroup.  A launch takes whole rounds of
+// one workgroup per CU, a round the longer the more a workgroup has to do; the shape with the
+// smallest product of the two is taken.  Measured for N = 256 .. 32768, T = 3 .. 64 and K =
+// 1792, 3584 and 7168 (256 CUs, weights from memory), on both sides of each border; us with
+// G x TT =              1 x 1   2 x 1   4 x 1   2 x 2   2 x 4
+//   16 x 4096  x 7168    13.8    16.9    24.7                     1 round of the smallest
+//   16 x 4224  x 7168    23.3    16.8    24.7                     2, 1 and 1 rounds
+//   16 x 8192  x 7168    24.9    18.2    25.7
+//   16 x 8320  x 7168    34.5    31.1    25.5                     3, 2 and 1
+//   16 x 16384 x 3584    24.9    18.5    16.8
+//   16 x 16640 x 3584    29.0    24.3    28.7                     5, 3 and 2
+//   32 x 2048  x 7168    13.1    16.2    23.7    23.3
+//   32 x 4096  x 7168    23.3    16.6    23.9    23.7
+//   32 x 4224  x 7168    32.8    28.1    24.2    23.8
+//   64 x 2048  x 7168    22.0    16.0    23.3    22.9    35.4
+//   64 x 4096  x 7168    41.4    28.6    23.7    23.2    35.8
+//   64 x 4224  x 7168    50.0    40.4    43.5    42.1    35.8
+//   64 x 16384 x 7168     157     106      88      86      72
+// Over all of these the taken shape is at most 12% behind the best (with 3 tokens, whose few
+// values make a round of 16 rows shorter than the rule counts), 0.8% on the average; with K of
+// 1024 7%, of 160, where a launch is 2 to 6 us and several workgroups run on a CU, 31%.  The sum
+// of an output is made in the same order by every shape.
 hipError_t launch_matvec_nvfp4(const MatvecArgs& a, hipStream_t stream) {
   if (a.T <= 2) {
-    const bool few = a.N < 8 * a.cus;
+    const bool few = a.N < 24 * a.cus;
     if (a.T == 1) return few ? launch_dot<1, 1, 8>(a, stream) : launch_dot<2, 1, 8>(a, stream);
     return few ? launch_dot<1, 2, 8>(a, stream) : launch_dot<2, 2, 8>(a, stream);
   }
-  const int fill = a.cus * 7 / 8;
-  const bool two = a.N >= 32 * fill;
-  const bool apart = ((a.N + 15) / 16) * ((a.T + 15) / 16) < a.cus * 7 / 4;
-  if (a.T <= 16 || apart) {
-    if (a.N >= 64 * fill) return launch_mfma<4, 1, 8>(a, stream);
-    return two ? launch_mfma<2, 1, 8>(a, stream) : launch_mfma<1, 1, 8>(a, stream);
-  }
-  if (a.T <= 32) return two ? launch_mfma<2, 2, 8>(a, stream) : launch_mfma<1, 2, 8>(a, stream);
-  return two ? launch_mfma<2, 4, 8>(a, stream) : launch_mfma<1, 4, 8>(a, stream);
+  auto cost = [&](int g, int tt, int round) {
+    const int groups = ((a.N + 16 * g - 1) / (16 * g)) * ((a.T + 16 * tt - 1) / (16 * tt));
+    return (groups + a.cus - 1) / a.cus * round;
+  };
+  const int c11 = cost(1, 1, 10), c21 = cost(2, 1, 11), c41 = cost(4, 1, 21);
+  const int c22 = cost(2, 2, 19), c24 = cost(2, 4, 30);
+  const int best = std::min({c11, c21, c41, c22, c24});
+  if (best == c11) return launch_mfma<1, 1, 8>(a, stream);
+  if (best == c21) return launch_mfma<2, 1, 8>(a, stream);
+  if (best == c41) return launch_mfma<4, 1, 8>(a, stream);
+  if (best == c22) return launch_mfma<2, 2, 8>(a, stream);
+  return launch_mfma<2, 4, 8>(a, stream);
 }
 
 }  // namespace rmoe

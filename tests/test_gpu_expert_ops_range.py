@@ -7,7 +7,7 @@ import torch
 import routed_moe_layer_amd as rm
 from tests import expert_ops as ref
 from tests.test_gpu_expert_ops import (KERNELS, _call, _check_grouped, _gen, _grouped_problem,
-                                       _guarded, _intact, _norm_check, _normal, _say)
+                                       _guarded, _intact, _matvec_check, _norm_check, _normal, _say)
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +126,30 @@ def test_grouped_gemm_situ_parameters_whose_product_leaves_fp32(q, R, E, N, K, b
     torch.cuda.synchronize()
     assert _intact(guard)
     _check_grouped(p, out)
+
+
+# ---------------------------------------------------------------------------------------
+# moe_matvec_nvfp4: sizes next to the borders between the shapes of workgroups (in rows per
+# CU, of which there are 256), and tokens that fill the LDS they are kept in
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("T,N,K", [
+    (1, 6143, 48), (1, 6144, 48), (2, 6143, 48), (2, 6144, 48),
+    (16, 4096, 144), (16, 4097, 144), (3, 8192, 144), (3, 8193, 144), (16, 16385, 144),
+    (32, 2048, 144), (32, 2049, 144), (17, 4097, 144), (32, 8193, 144), (64, 1024, 144),
+    (64, 1025, 144), (64, 2049, 144), (64, 4097, 144), (48, 8193, 144), (64, 12289, 160),
+    (1, 300, 32768), (2, 300, 16384), (1, 300, 32784), (2, 300, 16400)])
+def test_matvec_at_the_borders_of_its_shapes(T, N, K):
+    _say(f"matvec T={T} N={N} K={K}")
+    for f32 in (True, False):
+        _matvec_check(T, N, K, f32, seed=5)
+
+
+@pytest.mark.parametrize("N", [900, 2100, 4100, 8200, 16400])
+def test_matvec_of_a_token_does_not_depend_on_the_others(N):
+    """From three tokens on every shape adds an output's terms in the same order."""
+    _say(f"matvec slices N={N}")
+    x, codes, scales, alpha, y = _matvec_check(64, N, 304, True, seed=6)
+    for lo, n in ((0, 3), (7, 16), (20, 32), (16, 48)):
+        part = torch.empty((n, N), device="cuda")
+        rm.moe_matvec_nvfp4(n, N, 304, x[lo:lo + n], codes, scales, alpha, part, out_f32=True)
+        assert torch.equal(part, y[lo:lo + n])
