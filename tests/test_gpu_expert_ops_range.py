@@ -1,10 +1,12 @@
-"""GPU checks of the expert-stage operators at the ends of their types' ranges, against their
-definitions in 64 bits (tests/expert_ops.py)."""
+"""GPU checks of the expert-stage operators at the ends of their ranges (of the types, the sizes
+and the prefix sums) and of their stages on more tokens than one call of the logits takes,
+against their definitions in 64 bits (tests/expert_ops.py)."""
 
 import pytest
 import torch
 
 import routed_moe_layer_amd as rm
+import tests.test_gpu_expert_ops as ops
 from tests import expert_ops as ref
 from tests.test_gpu_expert_ops import (KERNELS, _call, _check_grouped, _gen, _grouped_problem,
                                        _guarded, _intact, _matvec_check, _norm_check, _normal, _say)
@@ -153,3 +155,39 @@ def test_matvec_of_a_token_does_not_depend_on_the_others(N):
         part = torch.empty((n, N), device="cuda")
         rm.moe_matvec_nvfp4(n, N, 304, x[lo:lo + n], codes, scales, alpha, part, out_f32=True)
         assert torch.equal(part, y[lo:lo + n])
+
+
+# ---------------------------------------------------------------------------------------
+# The E4M3 products as a whole, and the stages on more than 64 tokens
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("R,E,N,K", [(40, 1, 1100, 4096), (600, 1, 2000, 4096),
+                                     (20000, 3, 1000, 1024), (300, 4, 500, 8192)])
+def test_grouped_gemm_e4m3_sums_as_a_whole(R, E, N, K):
+    """Over many outputs the errors add like their squares.  A rounding to BF16 is off by at most
+    a uniform half step of 2^-7 of the value: rms 2^-7 / sqrt(12).  Seven products of eight are
+    cut below 2^-13 of the largest, uniformly and with either sign: rms 2^-13 / sqrt(3) of it,
+    whose square is at most the sum of the eight squares; over K / 8 groups that is 2^-13
+    sqrt(7 K / 3) of a product's rms, and the output's rms is sqrt(K) of it (the products are
+    independent with zero mean).  2% for the finite number of outputs."""
+    _say(f"grouped E4M3 rms R={R} E={E} N={N} K={K}")
+    p = _grouped_problem(R, E, N, K, "e4m3", False, False, "uniform", seed=31)
+    out, _ = _guarded(R, N)
+    _call(p, out)
+    want = ops._want(p)[0]
+    rms = ((2.0 ** -7) ** 2 / 12 + (2.0 ** -13) ** 2 * 7 / 3) ** 0.5
+    assert float((out.double() - want).norm() / want.norm()) <= 1.02 * rms
+
+
+@pytest.mark.parametrize("q,T,H,I,E,k", [("bf16", 150, 256, 64, 16, 4), ("int8", 129, 256, 64, 24, 2),
+                                         ("e4m3", 200, 256, 64, 16, 2)])
+def test_the_stages_together_on_more_tokens_than_one_call_of_logits(monkeypatch, q, T, H, I, E, k):
+    """The logits are made 64 tokens at a time."""
+    one = rm.moe_matvec_nvfp4
+
+    def slices(tokens, N, K, x, codes, scales, alpha, y, **kw):
+        for lo in range(0, tokens, rm.MOE_MATVEC_MAX_TOKENS):
+            part = slice(lo, min(lo + rm.MOE_MATVEC_MAX_TOKENS, tokens))
+            one(part.stop - lo, N, K, x[part], codes, scales, alpha, y[part], **kw)
+
+    monkeypatch.setattr(rm, "moe_matvec_nvfp4", slices)
+    ops.test_the_stages_together(q, T, H, I, E, k)
