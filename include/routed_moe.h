@@ -330,6 +330,9 @@ moe_status_t moe_topk_softmax(int32_t T, int32_t num_experts, int32_t top_k,
  * moe_route_v2 they make the whole layer:
  *   moe_rmsnorm -> moe_matvec_nvfp4 (logits) -> moe_topk_softmax -> moe_route ->
  *   moe_grouped_gemm (FC1, SiTU) -> moe_grouped_gemm (FC2) -> moe_combine.
+ * (Logits of more than MOE_MATVEC_MAX_TOKENS tokens are made that many at a time.  FC1's BF16
+ * rows become int8 rows for FC2 through moe_route_v2; nothing makes E4M3 rows of them, so FC2
+ * takes BF16 weights behind an E4M3 FC1.)
  * The conventions at the top of this file hold.  None of them needs a workspace, so calls
  * on different streams only need distinct outputs.
  * ------------------------------------------------------------------------------------ */
@@ -373,7 +376,8 @@ moe_status_t moe_matvec_nvfp4(int32_t T, int32_t N, int32_t K, const uint16_t* x
 
 /* Matrix products grouped by expert.  The R rows are sorted by expert: expert e owns rows
  * expert_cumsum[e-1] .. expert_cumsum[e] - 1 (the inclusive prefix sums moe_route writes);
- * rows at and past expert_cumsum[E-1] are left as they were.  With W_e = w[e], [Nw, K]:
+ * rows at and past expert_cumsum[E-1] are left as they were.  Prefix sums past [0, R] or
+ * falling ones write no other rows than those of out.  With W_e = w[e], [Nw, K]:
  *   h[i, n] = sum_k X[i, k] * W_e[n, k]
  *   out[i, n] = BF16(h[i, n]),                     Nw = N   (MOE_EPILOGUE_NONE)
  *   out[i, n] = BF16(SiTU(h[i, n], h[i, N + n])),  Nw = 2N  (MOE_EPILOGUE_SITU: rows [0, N)
@@ -407,7 +411,7 @@ moe_status_t moe_grouped_gemm(int32_t R, int32_t N, int32_t K, int32_t E, moe_qu
  * in fp32, j in order and add last; an index outside [0, R) (a dropped row: -1) is left out.
  * Buffers (device): rows BF16 [R, H]; expanded_row_idx i32 [T*k] (moe_route's gather map);
  * route_weights BF16 [T, k]; add BF16 [T, H] (the residual or a shared expert's output) or
- * NULL; out BF16 [T, H], may be the same buffer as add.
+ * NULL; out BF16 [T, H], may be the same buffer as add, not overlapping rows.
  * Limits: 1 <= T <= 2^21, T*k <= 2^24, 1 <= R <= 2^24, H % 8 == 0, 8 <= H <= 65536,
  * 1 <= k <= 64. */
 moe_status_t moe_combine(int32_t T, int32_t H, int32_t k, int32_t R, const uint16_t* rows,

@@ -332,7 +332,10 @@ struct Epilogue {
     }
     return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
-  // Store group c, or the adjacent groups c and c + 1.
+  // Store group c, or the adjacent groups c and c + 1.  Where N is no multiple of 4 a row's
+  // columns are not aligned to a group and go one by one, which costs the more the shorter K is:
+  // 64 experts x 512 rows, K = 512, int8, N = 3584 121 us, N = 3585 317 us; 8 experts x 4096
+  // rows, K = 4096, E4M3 414 and 584 us; 896 experts x 18 rows, K = 384, BF16 440 and 491 us.
   __device__ __forceinline__ void store(int c, int m, uint2 v) const {
     uint16_t* o = a.out + static_cast<int64_t>(row[m]) * a.N + n0[c];
     if (a.N % 4 == 0 && n0[c] + 4 <= a.N) {

@@ -2,9 +2,11 @@
 // as moe_quantize_nvfp4 writes them, one fp32 factor alpha):
 //   y[t, n] = alpha * sum_b S[n, b] * (sum_{i < 16} E2M1(W[n, 16b + i]) * x[t, 16b + i]).
 // Bound by the 9/16 byte per weight, and for the smallest by the latency of a launch: one
-// token x 16384 x 7168 (66 MB) 14.4 us, 4.6 TB/s; the router's logits, one token x 896 x 3584,
-// 3.2 us inside a graph.  With more tokens the token values, which every workgroup reads whole,
-// add to it: 16 tokens x 7181 x 7168 (29 MB) 15.0 us, 10.3 without their loads.  Two kernels:
+// token x 16384 x 7168 (66 MB) 14.3 us, 4.6 TB/s; the router's logits, one token x 896 x 3584,
+// 3.5 us inside a graph.  With more tokens the token values, which every workgroup reads whole,
+// add to it and soon bound it: 16 tokens x 7181 x 7168 (29 MB) 15.0 us, 10.3 without their
+// loads; 64 tokens x 16384 x 7168 72 us, with 470 MB of token values for 66 of weights.  Two
+// kernels:
 // with one or two tokens a wavefront takes whole weight rows, with more the matrix units take
 // 16 tokens at a time.
 #include <algorithm>
