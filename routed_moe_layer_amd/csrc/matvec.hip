@@ -269,8 +269,9 @@ static hipError_t launch_mfma(const MatvecArgs& a, hipStream_t stream) {
 // products (N = 7168 11.8 us against 12.6).
 //
 // More tokens: 16 G weight rows and 16 TT tokens per workgroup.  A launch takes whole rounds of
-// one workgroup per CU, a round the longer the more a workgroup has to do; the shape with the
-// smallest product of the two is taken.  Measured for N = 256 .. 32768, T = 3 .. 64 and K =
+// one workgroup per CU, a round the longer the more a workgroup has to do (10, 11, 21, 19 and 30
+// for the five shapes: fitted to all the times below); the shape with the smallest product of
+// the two is taken.  Measured for N = 256 .. 32768, T = 3 .. 64 and K =
 // 1792, 3584 and 7168 (256 CUs, weights from memory), on both sides of each border; us with
 // G x TT =              1 x 1   2 x 1   4 x 1   2 x 2   2 x 4
 //   16 x 4096  x 7168    13.8    16.9    24.7                     1 round of the smallest
