@@ -419,6 +419,90 @@ moe_status_t moe_combine(int32_t T, int32_t H, int32_t k, int32_t R, const uint1
                          const uint16_t* add, uint16_t* out, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * Microscaled FP4 (MXFP4) rows: a row of K values is K/2 bytes of E2M1 codes (element 2i in the
+ * low nibble of byte i) and one E8M0 scale byte per 32 values, 2^(byte - 127), 255 for NaN.  A
+ * row of scales is MOE_MXFP4_SCALE_STRIDE(K) bytes long, K/32 rounded up to whole dwords; the
+ * bytes past K/32 count for nothing as long as they are not 255 (moe_quantize_mxfp4 writes 0).
+ *   moe_quantize_mxfp4 -> moe_grouped_gemm_mxfp4 (FC1, SiTU) -> moe_quantize_mxfp4 ->
+ *   moe_grouped_gemm_mxfp4 (FC2) -> moe_combine
+ * is an expert layer in 4 bits behind moe_route, with weights quantized once.  None of the three
+ * needs a workspace.
+ * ------------------------------------------------------------------------------------ */
+#define MOE_MXFP4_SCALE_STRIDE(K) (((K) + 127) / 128 * 4)
+
+/* BF16 rows to MXFP4.  Per 32 consecutive values v: byte = max(floor(log2 max|v|) - 2 + 127, 0)
+ * (0 for a block of zeros), code = E2M1(v * 2^(127 - byte)), nearest even, saturating at 6, sign
+ * kept.  A block that holds a NaN or an infinity gets the byte 255 and codes 0.
+ * Buffers (device): src BF16 [rows, K]; codes u8 [rows, K/2]; scales u8 [rows,
+ * MOE_MXFP4_SCALE_STRIDE(K)].  Limits: rows >= 1, K % 32 == 0, 32 <= K <= 65536, rows *
+ * MOE_MXFP4_SCALE_STRIDE(K) / 4 < 2^31. */
+moe_status_t moe_quantize_mxfp4(const uint16_t* src, int64_t rows, int32_t K, uint8_t* codes,
+                                uint8_t* scales, moe_stream_t stream);
+
+/* The values of MXFP4 rows: out = BF16(E2M1(code) * 2^(byte - 127)), exact but for values past
+ * BF16's largest, which become infinite; NaN where the byte is 255.  Buffers and limits as
+ * above, out BF16 [rows, K]. */
+moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                  int32_t K, uint16_t* out, moe_stream_t stream);
+
+/* moe_grouped_gemm with both operands in MXFP4: rows, experts, prefix sums, source rows and the
+ * epilogue as there, with
+ *   h[i, n] = sum_b 2^(sx[b] - 127) 2^(sw[n, b] - 127) sum_{j < 32} X[i, 32b + j] W_e[n, 32b + j]
+ * over blocks b of K; the products of one block are added exactly, the blocks in fp32.
+ * Buffers (device): x_codes u8 [x_rows, K/2] and x_scales u8 [x_rows, MOE_MXFP4_SCALE_STRIDE(K)];
+ * w_codes u8 [E, Nw, K/2] and w_scales u8 [E, Nw, MOE_MXFP4_SCALE_STRIDE(K)]; row_idx,
+ * expert_cumsum, situ_beta, situ_linear_beta and out as at moe_grouped_gemm.
+ * Limits: 1 <= R, x_rows <= 2^24, 1 <= N <= 65536, K % 32 == 0, 32 <= K <= 65536,
+ * 1 <= E <= 10240, row_div >= 1. */
+moe_status_t moe_grouped_gemm_mxfp4(int32_t R, int32_t N, int32_t K, int32_t E,
+                                    moe_epilogue_t epilogue, const uint8_t* x_codes,
+                                    const uint8_t* x_scales, int32_t x_rows,
+                                    const int32_t* row_idx, int32_t row_div,
+                                    const int32_t* expert_cumsum, const uint8_t* w_codes,
+                                    const uint8_t* w_scales, const float* situ_beta,
+                                    const float* situ_linear_beta, uint16_t* out,
+                                    moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * How evenly a batch loads the experts, as a loss on the gate's probabilities, and its gradient
+ * for the router's logits.  With p[t] = softmax(logits[t]) over all experts and t over the
+ * tokens whose mask byte is not 0 (every token without a mask):
+ *   counts[e] = how many expert_ids[t, j] are e (ids outside [0, num_experts) count nowhere);
+ *   prob_sums[e] = sum_t p[t, e];  tokens = how many t;
+ *   loss = coef * num_experts * sum_e (counts[e] / sum counts) * (prob_sums[e] / tokens),
+ * 0 without a token or a counted id; an even load gives coef.  A logit of -inf is an expert that
+ * the token cannot take (p = 0; a row of them has p = 0 throughout); a NaN or +inf makes its
+ * row's p NaN.  Rows of masked tokens are not looked at, nor are their ids.
+ * moe_balance_loss_grad is the derivative with the counts held constant,
+ *   grad_logits[t, e] = g * coef * num_experts / (tokens * sum counts) * p[t, e] *
+ *                       (counts[e] - sum_i p[t, i] * counts[i]) + add[t, e]
+ * with g = *grad_loss (1 without), 0 + add for a masked token.  counts and tokens are
+ * moe_balance_loss's, or their sums over the ranks of a data-parallel batch; where they say that
+ * nothing was counted the gradient is add (0 without).
+ * Sums are fp32 or wider and in a fixed order: a call's result is the same every time.
+ * Buffers (device): logits f32 [T, num_experts], or BF16 with logits_are_bf16 != 0, and add (or
+ * NULL) and grad_logits of the same type; expert_ids i32 [T, top_k]; token_mask u8 [T] or NULL;
+ * counts i32 [num_experts]; prob_sums f32 [num_experts]; tokens i32 [1]; loss f32 [1]; grad_loss
+ * f32 [1] or NULL.  grad_logits may be the same buffer as add or logits.  workspace:
+ * moe_balance_workspace_size() bytes, 256-byte aligned, of any contents (the size grows with T
+ * and with num_experts only, so one for the largest call serves the smaller ones).
+ * Limits: 1 <= T <= 2^21, 1 <= num_experts <= 4096, 1 <= top_k <= 64, coef finite.
+ * ------------------------------------------------------------------------------------ */
+moe_status_t moe_balance_workspace_size(int32_t T, int32_t num_experts, size_t* bytes /*host*/);
+
+moe_status_t moe_balance_loss(int32_t T, int32_t num_experts, int32_t top_k, const void* logits,
+                              int32_t logits_are_bf16, const int32_t* expert_ids,
+                              const uint8_t* token_mask, float coef, int32_t* counts,
+                              float* prob_sums, int32_t* tokens, float* loss, void* workspace,
+                              size_t workspace_bytes, moe_stream_t stream);
+
+moe_status_t moe_balance_loss_grad(int32_t T, int32_t num_experts, const void* logits,
+                                   int32_t logits_are_bf16, const uint8_t* token_mask,
+                                   const int32_t* counts, const int32_t* tokens, float coef,
+                                   const float* grad_loss, const void* add, void* grad_logits,
+                                   moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Chunk-streamed front end, one rank ("[RFC] Chunk-ready symmetric-buffer protocol for
  * streaming MegaMoE inputs": sections "Fixed-capacity ring", "Independent readiness
  * generations", "Memory ordering", "Chunk-aware dispatch scheduling" options 1 --

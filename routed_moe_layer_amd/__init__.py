@@ -20,6 +20,9 @@ __all__ = [
     "moe_ring_publish", "moe_forward_streamed", "moe_sealed_workspace_size",
     "moe_forward_absorb", "moe_forward_seal", "moe_topk_softmax", "moe_forward_noalloc",
     "moe_rmsnorm", "moe_matvec_nvfp4", "moe_grouped_gemm", "moe_combine",
+    "moe_mxfp4_scale_stride", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
+    "moe_grouped_gemm_mxfp4", "moe_balance_workspace_size", "moe_balance_loss",
+    "moe_balance_loss_grad",
     "MOE_MATVEC_MAX_TOKENS", "MOE_EPILOGUE_NONE", "MOE_EPILOGUE_SITU",
     "MOE_QUANT_E4M3_ROW_DYNAMIC",
     "MOE_NOALLOC_SCRATCH_BYTES", "MOE_RING_ROUTE",
@@ -51,7 +54,8 @@ EXPORTED = ("moe_status_string", "moe_workspace_size", "moe_prepared_weights_siz
             "moe_ring_publish", "moe_forward_streamed", "moe_sealed_workspace_size",
             "moe_forward_absorb", "moe_forward_seal", "moe_topk_softmax",
             "moe_forward_noalloc", "moe_rmsnorm", "moe_matvec_nvfp4", "moe_grouped_gemm",
-            "moe_combine")
+            "moe_combine", "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_grouped_gemm_mxfp4",
+            "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_grad")
 
 MOE_RING_ROUTE = 0
 MOE_RING_LAYOUT = 1
@@ -149,6 +153,14 @@ def _lib():
             "moe_grouped_gemm": (st, [I32, I32, I32, I32, ctypes.c_int, ctypes.c_int, P, P, I32, P,
                                       I32, P, P, P, P, P, P, P]),
             "moe_combine": (st, [I32, I32, I32, I32, P, P, P, P, P, P]),
+            "moe_quantize_mxfp4": (st, [P, I64, I32, P, P, P]),
+            "moe_dequantize_mxfp4": (st, [P, P, I64, I32, P, P]),
+            "moe_grouped_gemm_mxfp4": (st, [I32, I32, I32, I32, ctypes.c_int, P, P, I32, P, I32, P,
+                                            P, P, P, P, P, P]),
+            "moe_balance_workspace_size": (st, [I32, I32, ctypes.POINTER(SZ)]),
+            "moe_balance_loss": (st, [I32, I32, I32, P, I32, P, P, ctypes.c_float, P, P, P, P, P,
+                                      SZ, P]),
+            "moe_balance_loss_grad": (st, [I32, I32, P, I32, P, P, P, ctypes.c_float, P, P, P, P]),
             "moe_forward_noalloc": (st, [MoeDims, I32, P, P, P, P, P, P, P, P, P, P, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -368,6 +380,10 @@ _KINDS = {
     "nvfp4": ("NVFP4 code bytes", "uint8 int8 float4_e2m1fn_x2"),
     "e4m3_scale": ("E4M3 scales", "uint8 float8_e4m3fn"),
     "byte": ("8 bits", "int8 uint8 float8_e4m3fn"),
+    "fp4": ("FP4 code bytes", "uint8 int8 float4_e2m1fn_x2"),
+    "e8m0": ("E8M0 scales", "uint8 float8_e8m0fnu"),
+    "mask": ("truth values", "bool uint8"),
+    "raw": ("bytes", "uint8 int8"),
 }
 _kind_types = {}
 
@@ -483,3 +499,80 @@ def moe_combine(T, H, k, R, rows, expanded_row_idx, route_weights, add, out, str
         ("out", out, T * H, "bf16"))
     _check("moe_combine", _lib().moe_combine(T, H, k, R, rows, expanded_row_idx, route_weights,
                                              add, out, stream))
+
+
+def moe_mxfp4_scale_stride(K):
+    """Bytes of a row of E8M0 scales: one per 32 values, rounded up to whole dwords."""
+    return (K + 127) // 128 * 4
+
+
+def moe_quantize_mxfp4(src, rows, K, codes, scales, stream=None):
+    stream, src, codes, scales = _checked(
+        "moe_quantize_mxfp4", stream, ("src", src, rows * K, "bf16"),
+        ("codes", codes, rows * K // 2, "fp4"),
+        ("scales", scales, rows * moe_mxfp4_scale_stride(K), "e8m0"))
+    _check("moe_quantize_mxfp4", _lib().moe_quantize_mxfp4(src, rows, K, codes, scales, stream))
+
+
+def moe_dequantize_mxfp4(codes, scales, rows, K, out, stream=None):
+    stream, codes, scales, out = _checked(
+        "moe_dequantize_mxfp4", stream, ("codes", codes, rows * K // 2, "fp4"),
+        ("scales", scales, rows * moe_mxfp4_scale_stride(K), "e8m0"),
+        ("out", out, rows * K, "bf16"))
+    _check("moe_dequantize_mxfp4", _lib().moe_dequantize_mxfp4(codes, scales, rows, K, out, stream))
+
+
+def moe_grouped_gemm_mxfp4(R, N, K, E, x_codes, x_scales, expert_cumsum, w_codes, w_scales, out,
+                           x_rows=None, row_idx=None, row_div=None, situ=False, situ_beta=None,
+                           situ_linear_beta=None, stream=None):
+    """``x_rows`` defaults to R; ``row_div`` counts with ``row_idx`` only."""
+    x_rows = R if x_rows is None else x_rows
+    row_div = 1 if row_idx is None or row_div is None else row_div
+    Nw, SB = 2 * N if situ else N, moe_mxfp4_scale_stride(K)
+    (stream, x_codes, x_scales, row_idx, expert_cumsum, w_codes, w_scales, situ_beta,
+     situ_linear_beta, out) = _checked(
+        "moe_grouped_gemm_mxfp4", stream, ("x_codes", x_codes, x_rows * K // 2, "fp4"),
+        ("x_scales", x_scales, x_rows * SB, "e8m0"), ("row_idx", row_idx, R, "i32"),
+        ("expert_cumsum", expert_cumsum, E, "i32"), ("w_codes", w_codes, E * Nw * K // 2, "fp4"),
+        ("w_scales", w_scales, E * Nw * SB, "e8m0"), ("situ_beta", situ_beta, E, "f32"),
+        ("situ_linear_beta", situ_linear_beta, E, "f32"), ("out", out, R * N, "bf16"))
+    _check("moe_grouped_gemm_mxfp4", _lib().moe_grouped_gemm_mxfp4(
+        R, N, K, E, MOE_EPILOGUE_SITU if situ else MOE_EPILOGUE_NONE, x_codes, x_scales, x_rows,
+        row_idx, row_div, expert_cumsum, w_codes, w_scales, situ_beta, situ_linear_beta, out,
+        stream))
+
+
+def moe_balance_workspace_size(T, num_experts):
+    n = ctypes.c_size_t()
+    _check("moe_balance_workspace_size",
+           _lib().moe_balance_workspace_size(T, num_experts, ctypes.byref(n)))
+    return n.value
+
+
+def moe_balance_loss(T, num_experts, top_k, logits, expert_ids, coef, counts, prob_sums, tokens,
+                     loss, workspace, token_mask=None, logits_bf16=False, workspace_bytes=None,
+                     stream=None):
+    nb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    (stream, logits, expert_ids, token_mask, counts, prob_sums, tokens, loss, workspace) = _checked(
+        "moe_balance_loss", stream,
+        ("logits", logits, T * num_experts, "bf16" if logits_bf16 else "f32"),
+        ("expert_ids", expert_ids, T * top_k, "i32"), ("token_mask", token_mask, T, "mask"),
+        ("counts", counts, num_experts, "i32"), ("prob_sums", prob_sums, num_experts, "f32"),
+        ("tokens", tokens, 1, "i32"), ("loss", loss, 1, "f32"), ("workspace", workspace, 0, "raw"))
+    _check("moe_balance_loss", _lib().moe_balance_loss(
+        T, num_experts, top_k, logits, int(logits_bf16), expert_ids, token_mask, coef, counts,
+        prob_sums, tokens, loss, workspace, nb, stream))
+
+
+def moe_balance_loss_grad(T, num_experts, logits, counts, tokens, coef, grad_logits,
+                          grad_loss=None, token_mask=None, add=None, logits_bf16=False,
+                          stream=None):
+    kind, n = "bf16" if logits_bf16 else "f32", T * num_experts
+    stream, logits, token_mask, counts, tokens, grad_loss, add, grad_logits = _checked(
+        "moe_balance_loss_grad", stream, ("logits", logits, n, kind),
+        ("token_mask", token_mask, T, "mask"), ("counts", counts, num_experts, "i32"),
+        ("tokens", tokens, 1, "i32"), ("grad_loss", grad_loss, 1, "f32"), ("add", add, n, kind),
+        ("grad_logits", grad_logits, n, kind))
+    _check("moe_balance_loss_grad", _lib().moe_balance_loss_grad(
+        T, num_experts, logits, int(logits_bf16), token_mask, counts, tokens, coef, grad_loss, add,
+        grad_logits, stream))

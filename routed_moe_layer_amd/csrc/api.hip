@@ -912,4 +912,159 @@ moe_status_t moe_combine(int32_t T, int32_t H, int32_t k, int32_t R, const uint1
   return hip_status(launch_combine(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
+static moe_status_t mx_rows(const void* bf16, int64_t rows, int32_t K, const uint8_t* codes,
+                            const uint8_t* scales, MxRowsArgs* a) {
+  if (rows < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (K % 32 || K > 65536 || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const int64_t units = (K + 127) / 128;
+  if (rows * units > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (!bf16 || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  if (!aligned(bf16, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  DeviceShape shape;
+  const moe_status_t st = device_shape(&shape);
+  if (st != MOE_OK) return st;
+  a->K = K;
+  a->units = static_cast<uint32_t>(units);
+  a->total = static_cast<uint32_t>(rows * units);
+  a->codes = const_cast<uint8_t*>(codes);
+  a->scales = const_cast<uint8_t*>(scales);
+  a->cus = shape.cus;
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_mxfp4(const uint16_t* src, int64_t rows, int32_t K, uint8_t* codes,
+                                uint8_t* scales, moe_stream_t stream) {
+  MxRowsArgs a{};
+  const moe_status_t st = mx_rows(src, rows, K, codes, scales, &a);
+  if (st != MOE_OK) return st;
+  a.src = src;
+  return hip_status(launch_quantize_mxfp4(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                  int32_t K, uint16_t* out, moe_stream_t stream) {
+  MxRowsArgs a{};
+  const moe_status_t st = mx_rows(out, rows, K, codes, scales, &a);
+  if (st != MOE_OK) return st;
+  a.out = out;
+  return hip_status(launch_dequantize_mxfp4(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm_mxfp4(int32_t R, int32_t N, int32_t K, int32_t E,
+                                    moe_epilogue_t epilogue, const uint8_t* x_codes,
+                                    const uint8_t* x_scales, int32_t x_rows,
+                                    const int32_t* row_idx, int32_t row_div,
+                                    const int32_t* expert_cumsum, const uint8_t* w_codes,
+                                    const uint8_t* w_scales, const float* situ_beta,
+                                    const float* situ_linear_beta, uint16_t* out,
+                                    moe_stream_t stream) {
+  if (epilogue != MOE_EPILOGUE_NONE && epilogue != MOE_EPILOGUE_SITU) return MOE_ERR_INVALID_ARG;
+  if (R < 1 || N < 1 || K < 1 || E < 1 || x_rows < 1 || row_div < 1) return MOE_ERR_INVALID_ARG;
+  const bool situ = epilogue == MOE_EPILOGUE_SITU;
+  if (R > kMaxGroupedRows || x_rows > kMaxGroupedRows || N > 65536 || K > 65536 || K % 32 ||
+      E > kRouteMaxExperts)
+    return MOE_ERR_UNSUPPORTED;
+  if (!x_codes || !x_scales || !expert_cumsum || !w_codes || !w_scales || !out)
+    return MOE_ERR_INVALID_ARG;
+  if (!situ && (situ_beta || situ_linear_beta)) return MOE_ERR_INVALID_ARG;
+  if (!row_idx && (x_rows < R || row_div != 1)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(out, 16) ||
+      !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(row_idx, 4) ||
+      !aligned(expert_cumsum, 4) || !aligned(situ_beta, 4) || !aligned(situ_linear_beta, 4))
+    return MOE_ERR_INVALID_ARG;
+  DeviceShape shape;
+  const moe_status_t st = device_shape(&shape);
+  if (st != MOE_OK) return st;
+  MxGroupedArgs a{};
+  a.R = R; a.N = N; a.Nw = situ ? 2 * N : N; a.E = E;
+  a.KB = K / 2; a.SB = MOE_MXFP4_SCALE_STRIDE(K);
+  a.situ = situ;
+  a.x = x_codes; a.x_mx = x_scales;
+  a.row_idx = row_idx; a.row_div = row_div; a.x_rows = x_rows;
+  a.cumsum = expert_cumsum;
+  a.w = w_codes; a.w_mx = w_scales;
+  a.beta = situ_beta; a.lam = situ_linear_beta;
+  a.out = out;
+  a.cus = shape.cus; a.xcds = shape.xcds;
+  return hip_status(launch_grouped_mxfp4(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+static moe_status_t balance_dims(int32_t T, int32_t num_experts) {
+  if (T < 1 || num_experts < 1) return MOE_ERR_INVALID_ARG;
+  return T > kMaxNormTokens || num_experts > 4096 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// The workspace of G parts of E experts; returns its bytes.
+static size_t balance_carve(int G, int E, uint8_t* base, BalanceArgs* a) {
+  Carver c;
+  const size_t joins = (static_cast<size_t>(E) + 63) / 64;
+  const size_t dot = c.take(joins * sizeof(double)), routed = c.take(joins * sizeof(int64_t));
+  const size_t ticket = c.take(sizeof(uint32_t)), tokens = c.take(static_cast<size_t>(G) * 4);
+  const size_t sums = c.take(static_cast<size_t>(G) * E * 4);
+  const size_t counts = c.take(static_cast<size_t>(G) * E * 4);
+  if (a) {
+    a->part_dot = reinterpret_cast<double*>(base + dot);
+    a->part_routed = reinterpret_cast<int64_t*>(base + routed);
+    a->ticket = reinterpret_cast<uint32_t*>(base + ticket);
+    a->part_tokens = reinterpret_cast<int32_t*>(base + tokens);
+    a->part_sums = reinterpret_cast<float*>(base + sums);
+    a->part_counts = reinterpret_cast<int32_t*>(base + counts);
+  }
+  return c.off;
+}
+
+moe_status_t moe_balance_workspace_size(int32_t T, int32_t num_experts, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = balance_dims(T, num_experts);
+  if (st != MOE_OK) return st;
+  *bytes = balance_carve(balance_parts(T, num_experts), num_experts, nullptr, nullptr);
+  return MOE_OK;
+}
+
+moe_status_t moe_balance_loss(int32_t T, int32_t num_experts, int32_t top_k, const void* logits,
+                              int32_t logits_are_bf16, const int32_t* expert_ids,
+                              const uint8_t* token_mask, float coef, int32_t* counts,
+                              float* prob_sums, int32_t* tokens, float* loss, void* workspace,
+                              size_t workspace_bytes, moe_stream_t stream) {
+  const moe_status_t st = balance_dims(T, num_experts);
+  if (st != MOE_OK) return st;
+  if (top_k < 1) return MOE_ERR_INVALID_ARG;
+  if (top_k > 64) return MOE_ERR_UNSUPPORTED;
+  if (!(coef >= -3.4e38f && coef <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (!logits || !expert_ids || !counts || !prob_sums || !tokens || !loss || !workspace)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, logits_are_bf16 ? 2 : 4) || !aligned(expert_ids, 4) ||
+      !aligned(counts, 4) || !aligned(prob_sums, 4) || !aligned(tokens, 4) || !aligned(loss, 4) ||
+      !aligned(workspace, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  BalanceArgs a{T, num_experts, top_k, logits, logits_are_bf16 != 0, expert_ids, token_mask, coef,
+                counts, prob_sums, tokens, loss, nullptr, nullptr, nullptr, nullptr, nullptr,
+                nullptr};
+  if (workspace_bytes < balance_carve(balance_parts(T, num_experts), num_experts,
+                                      static_cast<uint8_t*>(workspace), &a))
+    return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return hip_status(launch_balance_loss(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_balance_loss_grad(int32_t T, int32_t num_experts, const void* logits,
+                                   int32_t logits_are_bf16, const uint8_t* token_mask,
+                                   const int32_t* counts, const int32_t* tokens, float coef,
+                                   const float* grad_loss, const void* add, void* grad_logits,
+                                   moe_stream_t stream) {
+  moe_status_t st = balance_dims(T, num_experts);
+  if (st != MOE_OK) return st;
+  if (!(coef >= -3.4e38f && coef <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (!logits || !counts || !tokens || !grad_logits) return MOE_ERR_INVALID_ARG;
+  const size_t value = logits_are_bf16 ? 2 : 4;
+  if (!aligned(logits, value) || !aligned(counts, 4) || !aligned(tokens, 4) ||
+      !aligned(grad_loss, 4) || !aligned(add, value) || !aligned(grad_logits, value))
+    return MOE_ERR_INVALID_ARG;
+  DeviceShape shape;
+  st = device_shape(&shape);
+  if (st != MOE_OK) return st;
+  const BalanceGradArgs a{T, num_experts, logits, logits_are_bf16 != 0, token_mask, counts, tokens,
+                          coef, grad_loss, add, grad_logits, shape.cus};
+  return hip_status(launch_balance_loss_grad(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

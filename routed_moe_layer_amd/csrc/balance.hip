@@ -1,0 +1,458 @@
+// The router's balance: how evenly a batch loads the experts, as a loss on the gate's
+// probabilities, and its gradient.
+//   p[t] = softmax(logits[t]),  c_e = unmasked routed rows of expert e,  S_e = sum_t p[t, e],
+//   N = unmasked tokens,  loss = coef * E * sum_e (c_e / sum c) * (S_e / N);
+//   d loss / d logits[t, e] = coef * E / (N sum c) * p[t, e] * (c_e - sum_i p[t, i] c_i)
+// with the counts taken as constants.  The gradient uses c_e - mean(c), which changes nothing as
+// the probabilities sum to one: nearly equal counts keep their differences, equal ones give 0.
+//
+// A row is held in registers by LPR lanes (4, 16 or 64 by the number of experts), V values each,
+// so it is read once; the next row's loads are under way meanwhile.  The sums over tokens stay
+// in the same lanes, then go over the workgroup's wavefronts in LDS and over the workgroups in
+// a second launch, each in a fixed order, so a call's result never depends on timing.
+#include "common.h"
+#include "kernels.h"
+
+namespace rmoe {
+
+constexpr int kBalanceWaves = 8;
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dppf(float old, float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(x), CTRL,
+                                                    ROW_MASK, 0xF, false));
+}
+__device__ __forceinline__ float read_last(float x) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+// Maximum and sum over the LPR lanes of a row, returned to all of them.
+template <int LPR>
+__device__ __forceinline__ float row_max(float x) {
+  x = fmaxf(x, dppf<0xB1, 0xF>(x, x));                 // quad_perm [1,0,3,2]
+  x = fmaxf(x, dppf<0x4E, 0xF>(x, x));                 // quad_perm [2,3,0,1]
+  if constexpr (LPR >= 16) {
+    x = fmaxf(x, dppf<0x141, 0xF>(x, x));              // row_half_mirror
+    x = fmaxf(x, dppf<0x140, 0xF>(x, x));              // row_mirror
+  }
+  if constexpr (LPR == 64) {
+    x = fmaxf(x, dppf<0x142, 0xA>(x, x));              // row_bcast:15 into rows 1, 3
+    x = fmaxf(x, dppf<0x143, 0xC>(x, x));              // row_bcast:31 into rows 2, 3
+    x = read_last(x);
+  }
+  return x;
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+  x += dppf<0xB1, 0xF>(0.0f, x);
+  x += dppf<0x4E, 0xF>(0.0f, x);
+  if constexpr (LPR >= 16) {
+    x += dppf<0x141, 0xF>(0.0f, x);
+    x += dppf<0x140, 0xF>(0.0f, x);
+  }
+  if constexpr (LPR == 64) {
+    x += dppf<0x142, 0xA>(0.0f, x);
+    x += dppf<0x143, 0xC>(0.0f, x);
+    x = read_last(x);
+  }
+  return x;
+}
+
+// Expert of a lane's value v.  VEC: groups of four consecutive experts.
+template <int LPR, bool VEC>
+__device__ __forceinline__ int expert_of(int sub, int v) {
+  return VEC ? 4 * (sub + LPR * (v >> 2)) + (v & 3) : sub + LPR * v;
+}
+
+// A lane's V values of a row, `pad` past the last expert.  VEC needs E a multiple of 4 and rows
+// aligned to four values.
+template <bool BF16, int LPR, int V, bool VEC>
+__device__ __forceinline__ void load_row(const void* base, int64_t row, int E, int sub, float pad,
+                                         float (&z)[V]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const int e = 4 * (sub + LPR * i);
+      if (e < E) {
+        if constexpr (BF16) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + row * E + e);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            z[4 * i + 2 * j] = __uint_as_float(w[j] << 16);
+            z[4 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+          }
+        } else {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + row * E + e);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[4 * i + j] = w[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[4 * i + j] = pad;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = sub + LPR * v;
+      z[v] = pad;
+      if (e < E) {
+        if constexpr (BF16) z[v] = bf16_to_f32(static_cast<const uint16_t*>(base)[row * E + e]);
+        else z[v] = static_cast<const float*>(base)[row * E + e];
+      }
+    }
+  }
+}
+
+// exp(z - max) in place; returns 1 / their sum.  A row of -inf has probabilities 0 (factor 0); a
+// NaN or +inf makes the factor NaN.
+template <int LPR, int V>
+__device__ __forceinline__ float softmax_parts(float (&z)[V]) {
+  float m = z[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) m = fmaxf(m, z[v]);
+  m = row_max<LPR>(m);
+  if (m == -__builtin_inff()) m = 0.0f;
+  float s = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    z[v] = __builtin_amdgcn_exp2f((z[v] - m) * 1.4426950408889634f);
+    s += z[v];
+  }
+  s = row_sum<LPR>(s);
+  return s == 0.0f ? 0.0f : 1.0f / s;
+}
+
+template <bool BF16, int LPR, int V, bool VEC>
+__global__ __launch_bounds__(kBalanceWaves * 64, 2) void balance_stats_kernel(BalanceArgs a) {
+  constexpr int kRows = 64 / LPR;                      // rows per wavefront
+  extern __shared__ char s_raw[];
+  float* s_sum = reinterpret_cast<float*>(s_raw);
+  int32_t* s_count = reinterpret_cast<int32_t*>(s_raw) + a.E;
+  __shared__ int32_t s_tokens, s_routed;
+  __shared__ double s_dot[kBalanceWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, sub = lane % LPR;
+  constexpr int kThreads = kBalanceWaves * 64;
+  for (int e = tid; e < a.E; e += kThreads) {
+    s_sum[e] = 0.0f;
+    s_count[e] = 0;
+  }
+  if (tid == 0) s_tokens = s_routed = 0;
+  __syncthreads();
+
+  const int step = static_cast<int>(gridDim.x) * kBalanceWaves * kRows;
+  int t = (static_cast<int>(blockIdx.x) * kBalanceWaves + wave) * kRows + lane / LPR;
+  float z[V], acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+  auto counted = [&](int row) { return row < a.T && (!a.mask || a.mask[row]); };
+  // rows that do not count are never read
+  auto fetch = [&](int row, float (&to)[V]) {
+    if (counted(row)) {
+      load_row<BF16, LPR, V, VEC>(a.logits, row, a.E, sub, -__builtin_inff(), to);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) to[v] = -__builtin_inff();
+    }
+  };
+  fetch(t, z);
+  // the experts' counts, while the first rows are on their way
+  int tokens = 0;
+  const int ids = a.T * a.k;
+  for (int f = static_cast<int>(blockIdx.x) * kThreads + tid; f < ids; f += static_cast<int>(gridDim.x) * kThreads) {
+    const int row = f / a.k;
+    if (!counted(row)) continue;
+    if (f == row * a.k) ++tokens;
+    const int e = a.ids[f];
+    if (e >= 0 && e < a.E) atomicAdd(&s_count[e], 1);
+  }
+  if (tokens) atomicAdd(&s_tokens, tokens);
+  for (int base = t - lane / LPR; base < a.T; base += step, t += step) {   // whole wavefronts
+    float next[V];
+    fetch(t + step, next);
+    const float inv = softmax_parts<LPR, V>(z);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      acc[v] = __builtin_fmaf(z[v], inv, acc[v]);
+      z[v] = next[v];
+    }
+  }
+  if constexpr (LPR < 64) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int off = LPR; off < 64; off <<= 1) acc[v] += __shfl_xor(acc[v], off);
+    }
+  }
+  for (int w = 0; w < kBalanceWaves; ++w) {
+    if (wave == w && lane < LPR) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = expert_of<LPR, VEC>(sub, v);
+        if (e < a.E) s_sum[e] += acc[v];
+      }
+    }
+    __syncthreads();
+  }
+
+  if (gridDim.x > 1) {
+    float* sums = a.part_sums + static_cast<int64_t>(blockIdx.x) * a.E;
+    int32_t* counts = a.part_counts + static_cast<int64_t>(blockIdx.x) * a.E;
+    for (int e = tid; e < a.E; e += kThreads) {
+      sums[e] = s_sum[e];
+      counts[e] = s_count[e];
+    }
+    if (tid == 0) {
+      a.part_tokens[blockIdx.x] = s_tokens;
+      if (blockIdx.x == 0) *a.ticket = 0u;
+    }
+    return;
+  }
+  // one workgroup: it has everything
+  double dot = 0.0;
+  int routed = 0;
+  for (int e = tid; e < a.E; e += kThreads) {
+    const float s = s_sum[e];
+    const int c = s_count[e];
+    a.sums[e] = s;
+    a.counts[e] = c;
+    dot += static_cast<double>(c) * s;
+    routed += c;
+  }
+  if (routed) atomicAdd(&s_routed, routed);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
+  if (lane == 0) s_dot[wave] = dot;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kBalanceWaves; ++w) dot += s_dot[w];
+    const int n = s_tokens;
+    a.tokens[0] = n;
+    a.loss[0] = n > 0 && s_routed > 0
+                    ? static_cast<float>(static_cast<double>(a.coef) * a.E * dot /
+                                         (static_cast<double>(n) * s_routed))
+                    : 0.0f;
+  }
+}
+
+// The workgroups' sums and counts into the call's: 64 experts per workgroup, its sixteen
+// wavefronts over the G parts.  The workgroup that comes last adds up the loss.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(kJoinWaves * 64) void balance_join_kernel(BalanceArgs a, int G) {
+  __shared__ double s_sum[kJoinWaves][64];
+  __shared__ int32_t s_count[kJoinWaves][64];
+  __shared__ int32_t s_tokens[kJoinWaves];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int e = static_cast<int>(blockIdx.x) * 64 + lane;
+  double sum = 0.0;
+  int32_t count = 0;
+  if (e < a.E) {
+#pragma unroll 8
+    for (int g = wave; g < G; g += kJoinWaves) {
+      sum += a.part_sums[static_cast<int64_t>(g) * a.E + e];
+      count += a.part_counts[static_cast<int64_t>(g) * a.E + e];
+    }
+  }
+  s_sum[wave][lane] = sum;
+  s_count[wave][lane] = count;
+  int32_t tokens = 0;
+  if (blockIdx.x == 0) {
+    for (int g = threadIdx.x; g < G; g += kJoinWaves * 64) tokens += a.part_tokens[g];
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) tokens += __shfl_xor(tokens, off);
+    if (lane == 0) s_tokens[wave] = tokens;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    for (int w = 1; w < kJoinWaves; ++w) {
+      sum += s_sum[w][lane];
+      count += s_count[w][lane];
+    }
+    const float s = static_cast<float>(sum);
+    if (e < a.E) {
+      a.sums[e] = s;
+      a.counts[e] = count;
+    }
+    double dot = static_cast<double>(count) * s;
+    int64_t routed = count;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      dot += __shfl_xor(dot, off);
+      routed += __shfl_xor(routed, off);
+    }
+    if (lane == 0) {
+      a.part_dot[blockIdx.x] = dot;
+      a.part_routed[blockIdx.x] = routed;
+      if (blockIdx.x == 0) {
+        int32_t n = 0;
+        for (int w = 0; w < kJoinWaves; ++w) n += s_tokens[w];
+        a.tokens[0] = n;
+      }
+      __threadfence();
+      const bool last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+      __threadfence();
+      if (last) {
+        dot = 0.0;
+        routed = 0;
+        for (unsigned b = 0; b < gridDim.x; ++b) {
+          dot += __hip_atomic_load(a.part_dot + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          routed += __hip_atomic_load(a.part_routed + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        const int32_t n = __hip_atomic_load(a.tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        a.loss[0] = n > 0 && routed > 0
+                        ? static_cast<float>(static_cast<double>(a.coef) * a.E * dot /
+                                             (static_cast<double>(n) * static_cast<double>(routed)))
+                        : 0.0f;
+      }
+    }
+  }
+}
+
+template <bool BF16, int LPR, int V, bool VEC>
+__global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
+  constexpr int kRows = 64 / LPR;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = lane % LPR;
+  const int step = static_cast<int>(gridDim.x) * 4 * kRows;
+  int t = (static_cast<int>(blockIdx.x) * 4 + wave) * kRows + lane / LPR;
+  auto counted = [&](int row) { return row < a.T && (!a.mask || a.mask[row]); };
+  auto fetch = [&](int row, float (&to)[V]) {
+    if (counted(row)) {
+      load_row<BF16, LPR, V, VEC>(a.logits, row, a.E, sub, -__builtin_inff(), to);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) to[v] = -__builtin_inff();
+    }
+  };
+  float z[V], d[V];
+  fetch(t, z);
+  // centred counts
+  double all = 0.0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = expert_of<LPR, VEC>(sub, v);
+    if (e < a.E) all += a.counts[e];
+  }
+#pragma unroll
+  for (int off = 1; off < LPR; off <<= 1) all += __shfl_xor(all, off);
+  const double mean = all / a.E;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = expert_of<LPR, VEC>(sub, v);
+    d[v] = e < a.E ? static_cast<float>(a.counts[e] - mean) : 0.0f;
+  }
+  const double n = a.tokens[0];
+  const float scale = n > 0.0 && all > 0.0
+                          ? static_cast<float>(static_cast<double>(a.coef) * a.E / (n * all)) *
+                                (a.grad_loss ? a.grad_loss[0] : 1.0f)
+                          : 0.0f;
+  for (int base = t - lane / LPR; base < a.T; base += step, t += step) {   // whole wavefronts
+    float next[V], more[V];
+    if (a.add && t < a.T) {
+      load_row<BF16, LPR, V, VEC>(a.add, t, a.E, sub, 0.0f, more);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) more[v] = 0.0f;
+    }
+    fetch(t + step, next);
+    const float inv = softmax_parts<LPR, V>(z);
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) dot = __builtin_fmaf(z[v], d[v], dot);
+    dot = row_sum<LPR>(dot) * inv;
+    if (t < a.T) {
+      const float f = scale * inv;
+      const bool live = counted(t);
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        o[v] = live ? __builtin_fmaf(f * z[v], d[v] - dot, more[v]) : more[v];
+      const int64_t at = static_cast<int64_t>(t) * a.E;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          const int e = 4 * (sub + LPR * i);
+          if (e >= a.E) continue;
+          if constexpr (BF16)
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.grad) + at + e) =
+                u32x2{pack_bf16x2(o[4 * i], o[4 * i + 1]), pack_bf16x2(o[4 * i + 2], o[4 * i + 3])};
+          else
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.grad) + at + e) =
+                f32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int e = sub + LPR * v;
+          if (e >= a.E) continue;
+          if constexpr (BF16) static_cast<uint16_t*>(a.grad)[at + e] = f32_to_bf16(o[v]);
+          else static_cast<float*>(a.grad)[at + e] = o[v];
+        }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) z[v] = next[v];
+  }
+}
+
+// f(IntC<LPR>, IntC<V>) for the lanes and registers that a row of E experts takes.
+template <int V>
+struct RowC { static constexpr int value = V; };
+template <class F>
+static void for_experts(int E, F f) {
+  if (E <= 16) f(RowC<4>{}, RowC<4>{});
+  else if (E <= 64) f(RowC<16>{}, RowC<4>{});
+  else if (E <= 256) f(RowC<64>{}, RowC<4>{});
+  else if (E <= 512) f(RowC<64>{}, RowC<8>{});
+  else if (E <= 1024) f(RowC<64>{}, RowC<16>{});
+  else if (E <= 2048) f(RowC<64>{}, RowC<32>{});
+  else f(RowC<64>{}, RowC<64>{});
+}
+
+int balance_parts(int T, int E) {
+  const int rows = kBalanceWaves * (E <= 16 ? 16 : E <= 64 ? 4 : 1);
+  const int G = (T + rows - 1) / rows;
+  return G < kBalanceMaxParts ? G : kBalanceMaxParts;
+}
+
+hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream) {
+  const int G = balance_parts(a.T, a.E);
+  const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (a.bf16 ? 8 : 16) == 0;
+  const size_t lds = static_cast<size_t>(a.E) * 8;
+  for_experts(a.E, [&](auto lpr, auto v) {
+    constexpr int L = decltype(lpr)::value, V = decltype(v)::value;
+    const dim3 grid(static_cast<unsigned>(G)), block(kBalanceWaves * 64);
+    if (a.bf16) {
+      if (vec) balance_stats_kernel<true, L, V, true><<<grid, block, lds, stream>>>(a);
+      else balance_stats_kernel<true, L, V, false><<<grid, block, lds, stream>>>(a);
+    } else {
+      if (vec) balance_stats_kernel<false, L, V, true><<<grid, block, lds, stream>>>(a);
+      else balance_stats_kernel<false, L, V, false><<<grid, block, lds, stream>>>(a);
+    }
+  });
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || G == 1) return err;
+  balance_join_kernel<<<dim3(static_cast<unsigned>((a.E + 63) / 64)), dim3(kJoinWaves * 64), 0,
+                        stream>>>(a, G);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_loss_grad(const BalanceGradArgs& a, hipStream_t stream) {
+  const int rows = 4 * (a.E <= 16 ? 16 : a.E <= 64 ? 4 : 1);
+  const int blocks = (a.T + rows - 1) / rows, most = 8 * a.cus;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.add) |
+                        reinterpret_cast<uintptr_t>(a.grad);
+  const bool vec = a.E % 4 == 0 && all % (a.bf16 ? 8 : 16) == 0;
+  for_experts(a.E, [&](auto lpr, auto v) {
+    constexpr int L = decltype(lpr)::value, V = decltype(v)::value;
+    const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most)), block(256);
+    if (a.bf16) {
+      if (vec) balance_grad_kernel<true, L, V, true><<<grid, block, 0, stream>>>(a);
+      else balance_grad_kernel<true, L, V, false><<<grid, block, 0, stream>>>(a);
+    } else {
+      if (vec) balance_grad_kernel<false, L, V, true><<<grid, block, 0, stream>>>(a);
+      else balance_grad_kernel<false, L, V, false><<<grid, block, 0, stream>>>(a);
+    }
+  });
+  return hipGetLastError();
+}
+
+}  // namespace rmoe

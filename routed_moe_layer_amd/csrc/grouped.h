@@ -12,6 +12,37 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 template <int V>
 struct IntC { static constexpr int value = V; };
 
+// Sixteen zero bytes: what a lane loads in the place of bytes past the end of K.
+__device__ const u32x4 g_zero16 = {0u, 0u, 0u, 0u};
+
+typedef const __attribute__((address_space(1))) void* global_ptr;
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// The wave's 64 x 16 bytes from each lane's address into consecutive LDS bytes, or 64 x 4.
+__device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void load4_to_lds(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)dst, 4, 0, 0);
+}
+
+// A buffer of a ring beyond its first three.
+template <int U, int BYTES>
+__device__ __forceinline__ uint8_t* more_ring() {
+  __shared__ alignas(16) uint8_t s_more[BYTES];
+  return s_more;
+}
+
+// f(IntC<0>), ..., f(IntC<S - 1>).
+template <int S, int U = 0, class F>
+__device__ __forceinline__ void for_ring(F f) {
+  f(IntC<U>{});
+  if constexpr (U + 1 < S) for_ring<S, U + 1>(f);
+}
+
+// The s_waitcnt operand for at most vm vector memory operations under way and no LDS one.
+constexpr int wait_vm_lds(int vm) { return (vm & 15) | 0x70 | (vm >> 4) << 14; }
+
 // Operand types by their moe_quant_t value: 0 BF16, 1 int8, 3 E4M3.
 template <int Q> struct AccOf { typedef f32x4 type; };
 template <> struct AccOf<1> { typedef i32x4 type; };

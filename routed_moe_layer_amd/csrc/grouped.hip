@@ -20,34 +20,6 @@ namespace rmoe {
 template <int Q>
 using acc_t = typename AccOf<Q>::type;
 
-// Sixteen zero bytes: what a lane loads in the place of bytes past the end of K.
-__device__ const u32x4 g_zero16 = {0u, 0u, 0u, 0u};
-
-typedef const __attribute__((address_space(1))) void* global_ptr;
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
-// The wave's 64 x 16 bytes from each lane's address into consecutive LDS bytes.
-__device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* dst) {
-  __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)dst, 16, 0, 0);
-}
-
-// A buffer of a ring beyond its first three.
-template <int U, int BYTES>
-__device__ __forceinline__ uint8_t* more_ring() {
-  __shared__ alignas(16) uint8_t s_more[BYTES];
-  return s_more;
-}
-
-// f(IntC<0>), ..., f(IntC<S - 1>).
-template <int S, int U = 0, class F>
-__device__ __forceinline__ void for_ring(F f) {
-  f(IntC<U>{});
-  if constexpr (U + 1 < S) for_ring<S, U + 1>(f);
-}
-
-// The s_waitcnt operand for at most vm vector memory operations under way and no LDS one.
-constexpr int wait_vm_lds(int vm) { return (vm & 15) | 0x70 | (vm >> 4) << 14; }
-
 // ---------------------------------------------------------------------------------------
 // Tiles of up to BM rows (32, 64 or 128).  A workgroup of NW wavefronts multiplies one tile of
 // an expert's rows with 32 NW weight rows, 32 per wavefront.  Both operands go from memory

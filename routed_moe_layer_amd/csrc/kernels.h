@@ -220,6 +220,66 @@ struct GroupedArgs {
 };
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
 
+// Products grouped by expert of microscaled FP4 rows (grouped_mxfp4.hip): KB = K/2 code bytes,
+// scales in rows of SB bytes.
+struct MxGroupedArgs : GroupedArgs {
+  const uint8_t* x_mx;         // [x_rows, SB] E8M0
+  const uint8_t* w_mx;         // [E, Nw, SB]
+  int SB;                      // a multiple of 4, at least K/32
+};
+hipError_t launch_grouped_mxfp4(const MxGroupedArgs& a, hipStream_t stream);
+
+// Microscaled FP4 rows and back (mxfp4.hip).
+struct MxRowsArgs {
+  int K;                       // a multiple of 32
+  uint32_t units, total;       // dwords of scales in a row (128 values each), in all rows
+  const uint16_t* src;         // [rows, K] BF16 (quantize)
+  uint8_t* codes;              // [rows, K/2]
+  uint8_t* scales;             // [rows, 4 * units] E8M0
+  uint16_t* out;               // [rows, K] BF16 (dequantize)
+  int cus;
+};
+hipError_t launch_quantize_mxfp4(const MxRowsArgs& a, hipStream_t stream);
+hipError_t launch_dequantize_mxfp4(const MxRowsArgs& a, hipStream_t stream);
+
+// The router's balance loss and its gradient (balance.hip).
+constexpr int kBalanceMaxParts = 512;
+struct BalanceArgs {
+  int T, E, k;
+  const void* logits;          // [T, E] fp32 or BF16
+  int bf16;
+  const int32_t* ids;          // [T, k]
+  const uint8_t* mask;         // [T] or null
+  float coef;
+  int32_t* counts;             // [E]
+  float* sums;                 // [E]
+  int32_t* tokens;             // [1]
+  float* loss;                 // [1]
+  // one part per workgroup of the first launch (balance_parts), one dot product per workgroup
+  // of the second
+  float* part_sums;
+  int32_t *part_counts, *part_tokens;
+  double* part_dot;
+  int64_t* part_routed;
+  uint32_t* ticket;
+};
+int balance_parts(int T, int E);
+hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream);
+struct BalanceGradArgs {
+  int T, E;
+  const void* logits;          // [T, E] fp32 or BF16, add and grad alike
+  int bf16;
+  const uint8_t* mask;         // [T] or null
+  const int32_t* counts;       // [E]
+  const int32_t* tokens;       // [1]
+  float coef;
+  const float* grad_loss;      // [1] or null
+  const void* add;             // or null
+  void* grad;
+  int cus;
+};
+hipError_t launch_balance_loss_grad(const BalanceGradArgs& a, hipStream_t stream);
+
 // Weighted sum of expert rows into tokens (combine.hip).
 struct CombineArgs {
   int64_t T, R;
