@@ -46,6 +46,32 @@ __device__ __forceinline__ f32x4 mx_mma(u32x4 a, u32x4 b, f32x4 acc, uint32_t sa
                                                           F, static_cast<int>(sb));
 }
 
+// Eight consecutive columns n .. n + 7 of a row at o, those below N.  Where N is no multiple of 8 a
+// row's columns are aligned to four or to one of them.
+__device__ __forceinline__ void store_columns(uint16_t* o, u32x4 v, int N, int n) {
+  if (N % 8 == 0) {
+    if (n < N) *reinterpret_cast<u32x4*>(o) = v;
+  } else if (N % 4 == 0) {
+    if (n < N) *reinterpret_cast<uint2*>(o) = make_uint2(v[0], v[1]);
+    if (n + 4 < N) *reinterpret_cast<uint2*>(o + 4) = make_uint2(v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (n + i < N) o[i] = static_cast<uint16_t>(v[i >> 1] >> (16 * (i & 1)));
+  }
+}
+// The same for four columns.
+__device__ __forceinline__ void store_columns(uint16_t* o, uint2 v, int N, int n) {
+  if (N % 4 == 0) {
+    if (n < N) *reinterpret_cast<uint2*>(o) = v;
+  } else {
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
 // The same with the accumulator in place in AGPRs.  The builtin's result may go to other registers
 // than its addend: with 256 of them in use that took 300 register moves per 256 products, and
 // spills.  Written out, the instruction's waits are not the compiler's: an operand must not come
@@ -62,21 +88,6 @@ __device__ __forceinline__ void mx_mma_in_place(u32x4 a, u32x4 b, f32x4& acc, ui
   else RMOE_MX_MMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
 #undef RMOE_MX_MMA
 }
-// Eight consecutive columns n .. n + 7 of a row at o, those below N.  Where N is no multiple of 8 a
-// row's columns are aligned to four or to one of them.
-__device__ __forceinline__ void store_columns(uint16_t* o, u32x4 v, int N, int n) {
-  if (N % 8 == 0 && n < N) {
-    *reinterpret_cast<u32x4*>(o) = v;
-  } else if (N % 4 == 0) {
-    if (n < N) *reinterpret_cast<uint2*>(o) = make_uint2(v[0], v[1]);
-    if (n + 4 < N) *reinterpret_cast<uint2*>(o + 4) = make_uint2(v[2], v[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (n + i < N) o[i] = static_cast<uint16_t>(v[i >> 1] >> (16 * (i & 1)));
-  }
-}
-
 // Before a batch of them whose operands vector instructions may have written, two wait states.
 // (Inside a batch only LDS reads write operands, which are waited for.  An s_nop in front of each
 // instruction took 4% of 8192^3.)
@@ -85,21 +96,162 @@ __device__ __forceinline__ void ready() { asm volatile("s_nop 1" ::: "memory"); 
 // after 7 wait states, and code behind the loop may read it at once.
 __device__ __forceinline__ void settle() { asm volatile("s_nop 7" ::: "memory"); }
 
+// The last i with s[i] <= v, for rising s[0 .. n] with s[0] <= v < s[n], n <= 2^18: 64 entries at a
+// time are looked at by the lanes, so that a search is two or three LDS reads long.
+__device__ __forceinline__ int mx_last_at_most(const int32_t* s, int n, int v) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, step = n > 4096 ? 4096 : n > 64 ? 64 : 1;
+  for (;;) {
+    const int i = lo + lane * step;
+    const uint64_t in = __ballot(i < n && s[i] <= v);  // a run of lanes from 0 on
+    lo += (__popcll(in) - 1) * step;
+    if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
+    step /= 64;
+  }
+}
+
+// scan_experts with the prefix sums read eight at a time: a workgroup of one or two wavefronts
+// takes several rounds of them, and the latency of each is part of a small call's time.
+template <int NW, class F>
+__device__ __forceinline__ void mx_scan(const GroupedArgs& a, int32_t* s, int32_t most, F count) {
+  constexpr int kThreads = NW * 64, kBatch = 8;
+  for (int base = 0; base < a.E; base += kThreads * kBatch) {
+    int32_t end[kBatch], begin[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = base + i * kThreads + static_cast<int>(threadIdx.x);
+      end[i] = e < a.E ? a.cumsum[e] : 0;
+      begin[i] = e > 0 && e < a.E ? a.cumsum[e - 1] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = base + i * kThreads + static_cast<int>(threadIdx.x);
+      const int lo = min(max(begin[i], 0), a.R), hi = min(max(end[i], lo), a.R);
+      if (e < a.E) s[e] = count(hi - lo);
+    }
+  }
+  __syncthreads();
+  __shared__ int32_t s_wave[NW];
+  const int per = (a.E + kThreads - 1) / kThreads;
+  const int lo = min(static_cast<int>(threadIdx.x) * per, a.E), hi = min(lo + per, a.E);
+  int sum = 0;
+  for (int e = lo; e < hi; ++e) sum += s[e];
+  sum = min(sum, most);                  // (a cut part alone brings every later sum to the cut)
+  int inc = sum;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int v = __shfl_up(inc, off);
+    if (lane >= off) inc += v;
+  }
+  if (lane == 63) s_wave[wave] = inc;
+  __syncthreads();
+  int before = inc - sum;
+  for (int i = 0; i < wave; ++i) before += s_wave[i];
+  for (int e = lo; e < hi; ++e) {
+    const int n = s[e];
+    s[e] = min(before, most);
+    before += n;
+  }
+  if (threadIdx.x == kThreads - 1) s[a.E] = min(before, most);
+  __syncthreads();
+}
+
+// Rows of expert e, the same for the whole wavefront, as expert_rows.  They come by scalar loads:
+// a wait for vector ones would be one for all the loads under way.
+__device__ __forceinline__ int2 mx_expert_rows(const GroupedArgs& a, int e) {
+  typedef const __attribute__((address_space(4))) int32_t* ScalarPtr;
+  const ScalarPtr cumsum = (ScalarPtr)a.cumsum;
+  const int lo = e > 0 ? min(max(cumsum[e - 1], 0), a.R) : 0;
+  return make_int2(lo, min(max(cumsum[e], lo), a.R));
+}
+
+// The source row of an entry of row_idx, or -1, as source_row.
+__device__ __forceinline__ int64_t source_of(const GroupedArgs& a, int s) {
+  if (s < 0) return -1;
+  if (a.row_div > 1) s = static_cast<int>(static_cast<uint32_t>(s) / static_cast<uint32_t>(a.row_div));
+  return s < a.x_rows ? s : -1;
+}
+
+// The work items of a persistent workgroup, a tile and one block of weight rows each, in the order
+// of ItemWalk: runs of kTileRun tiles, inside a run by weight block, inside a block by tile, runs
+// dealt to the XCDs in turn or in equal contiguous parts.  There are fewer than 2^31 (at most 2^17 +
+// 1536 tiles x 512 blocks, 2^18 + 10240 x 1024 or, of the smallest tiles, which few rows take,
+// 2^15 x 2048), and a step is made without a division.
+struct MxItemWalk {
+  int tiles, nblk, xcd, step, run, rem, left;
+  bool deal;
+  __device__ __forceinline__ MxItemWalk(const GroupedArgs& a, int all_tiles, int blocks)
+      : tiles(all_tiles), nblk(blocks) {
+    xcd = static_cast<int>(blockIdx.x) % a.xcds;
+    step = static_cast<int>(gridDim.x) / a.xcds;
+    const int first = static_cast<int>(blockIdx.x) / a.xcds, per_run = kTileRun * nblk;
+    const int runs = (tiles + kTileRun - 1) / kTileRun;
+    deal = runs >= kDealRuns * a.xcds;
+    int at = first;
+    if (deal) {
+      left = (runs - xcd + a.xcds - 1) / a.xcds * per_run - first;
+    } else {
+      const int64_t total = static_cast<int64_t>(tiles) * nblk;
+      const int begin = static_cast<int>(total * xcd / a.xcds);
+      left = static_cast<int>(total * (xcd + 1) / a.xcds) - begin - first;
+      at += begin;
+    }
+    run = at / per_run;
+    rem = at - run * per_run;
+  }
+  // The next item: its tile and weight block; false when there is none left.
+  __device__ __forceinline__ bool next(int xcds, int* tile, int* cb) {
+    const int per_run = kTileRun * nblk;
+    while (left > 0) {
+      const int r = deal ? run * xcds + xcd : run, m = rem;
+      left -= step;
+      rem += step;
+      while (rem >= per_run) {
+        rem -= per_run;
+        ++run;
+      }
+      const int in_run = min(kTileRun, tiles - r * kTileRun);
+      if (m >= in_run * nblk) continue;                // the last run may be short
+      *cb = in_run == kTileRun ? m / kTileRun : m / in_run;
+      *tile = r * kTileRun + (m - *cb * in_run);
+      return true;
+    }
+    return false;
+  }
+};
+
 // ---------------------------------------------------------------------------------------
-// Tiles of up to BM rows (32, 64 or 128).  A workgroup of NW wavefronts multiplies one tile of
+// Tiles of up to BM rows (16, 32, 64 or 128).  A workgroup of NW wavefronts multiplies one tile of
 // an expert's rows with 32 NW weight rows, 32 per wavefront.  Codes and scales of both operands
-// go from memory straight into LDS in chunks, in a ring of S chunks that runs on over the border
-// between two items.  Every wavefront issues the same number of loads per chunk (the token rows'
-// scales are loaded by several wavefronts alike), so one counted wait per chunk is enough: a
-// chunk is there when no more loads are under way than were issued after it.
+// go from memory straight into LDS in chunks of 128 bytes of K, in a ring of S chunks that runs on
+// over the borders between items: the load side is S - 1 chunks ahead of the products, with items
+// of its own.  Every wavefront issues the same number of loads per chunk (the token rows' scales
+// are loaded by several wavefronts alike), so one counted wait per chunk is enough: a chunk is
+// there when no more loads are under way than were issued after it (stores behind them only make
+// it wait for more).
+//
+// Bound by the bytes: FC1 of 16 tokens over 896 experts (N = 384 with SiTU, K = 3584, 328 MB) 71
+// us, 4.6 TB/s; FC1 of 4096 tokens (1.37 GB) 345 us, 4.0 TB/s; FC2 of 1024 Zipf tokens (N = 3584,
+// K = 384, 763 MB) 209 us, 3.6 TB/s, two chunks an item, half of the second of them zeros; a large
+// read on the same card 5.99 TB/s.  A CU takes in about 20 bytes a ns this way, whether they come
+// from memory or from a cache, and the token rows' count with the weights'.  Eight wavefronts per
+// CU are needed for that: longer rings with four took 76 to 101 us for the 71.
 // ---------------------------------------------------------------------------------------
-template <bool SITU, int BM, int NW, int PER_CU, int S>
-__global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mx_mid_kernel(MxGroupedArgs a) {
-  constexpr int kRows = 32 * NW, kCols = kRows / (SITU ? 2 : 1);
+//
+// DIRECT: the source rows of a tile are read from row_idx, which the wavefront has to wait for
+// with the loads around them.  Otherwise they are the sorted rows themselves or, of at most
+// kMxListRows, in a list in LDS.
+constexpr int kMxListRows = 2048;
+
+template <bool SITU, bool DIRECT, int BM, int NW, int PER_CU, int S>
+__global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid_kernel(MxGroupedArgs a) {
+  constexpr int kRows = 32 * NW, kCols = kRows / (SITU ? 2 : 1), MT = BM / 16;
   constexpr int kXLoads = BM / (8 * NW), kLoads = 6 + kXLoads;       // per wavefront and chunk
-  static_assert(kXLoads * 8 * NW == BM && BM / 32 <= NW, "");
+  constexpr int kXScaleLoads = BM < 32 ? 1 : BM / 32;                // of 32 rows
+  static_assert(kXLoads * 8 * NW == BM && kXScaleLoads <= NW, "");
   // a buffer: weights, token rows, the weights' scales, the token rows' scales
-  constexpr int kScales = (kRows + BM) * 128, kBytes = (kRows + BM) * 136;
+  constexpr int kScales = (kRows + BM) * 128, kBytes = kScales + (kRows + 32 * kXScaleLoads) * 8;
   extern __shared__ int32_t s_tile[];
   __shared__ alignas(16) uint8_t s_0[kBytes], s_1[kBytes], s_2[kBytes];
   auto ring = [&](auto u) {
@@ -109,94 +261,150 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mx_mid_kerne
     else if constexpr (U == 2) return &s_2[0];
     else return more_ring<U, kBytes>();
   };
-  scan_experts<NW>(a, s_tile, a.R / BM + min(a.R, a.E), [](int n) { return (n + BM - 1) / BM; });
+  mx_scan<NW>(a, s_tile, a.R / BM + min(a.R, a.E), [](int n) { return (n + BM - 1) / BM; });
   const int nblk = (a.N + kCols - 1) / kCols;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int g = lane >> 4, l16 = lane & 15;
   const int KB = a.KB, SB = a.SB;
-  // an item takes whole rounds of the ring (chunks past the end of K are zeros), so that every
-  // item starts with the first buffers
-  const int nc = (KB + 128 * S - 1) / (128 * S) * S;
-  const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero16);
-  ItemWalk walk(a, s_tile, nblk);
-  TileRows ld;
-  int ld_cb = 0;
-  bool more = walk.next<BM>(&ld, &ld_cb);
-  if (!more) return;                                   // the whole workgroup
+  const int nc = max((KB + 127) / 128, 2);             // (chunks past the end of K are zeros)
+  int32_t* s_source = s_tile + a.E + 1;                // the list
+  if (!DIRECT && a.row_idx) {
+    for (int i = tid; i < a.R; i += NW * 64) s_source[i] = static_cast<int32_t>(source_row(a, i));
+    __syncthreads();
+  }
+  const uint8_t *zero = reinterpret_cast<const uint8_t*>(&g_zero16),
+                *zeros = reinterpret_cast<const uint8_t*>(g_zero_row);
+
+  // An expert's rows are dealt evenly to its tiles in multiples of 16 (find_tile_even); the last
+  // tiles of an expert may hold no row.
+  struct Item {
+    int expert, row0, nrows, cb;
+  };
+  auto next_item = [&](MxItemWalk& walk, Item* it) __attribute__((always_inline)) {
+    int tile;
+    while (walk.next(a.xcds, &tile, &it->cb)) {
+      const int e = mx_last_at_most(s_tile, a.E, tile);
+      const int2 r = mx_expert_rows(a, e);
+      const int cnt = r.y - r.x, nt = (cnt + BM - 1) / BM;
+      const int per = nt == 1 ? BM : ((cnt + nt - 1) / nt + 15) / 16 * 16;
+      it->expert = e;
+      it->row0 = r.x + (tile - s_tile[e]) * per;
+      it->nrows = min(per, r.y - it->row0);
+      if (it->nrows > 0) return true;
+    }
+    return false;
+  };
+  MxItemWalk load_walk(a, s_tile[a.E], nblk), walk = load_walk;
+  Item ld, it;
+  if (!next_item(walk, &it)) return;                   // the whole workgroup
 
   // Load j of a wavefront fills rows 8 j + lane / 8 of its 32 weight rows, or of its token rows,
   // slot lane % 8 of a row with piece (lane % 8) ^ mx_swizzle(row).  A load of scales takes 32
   // rows, two lanes each.
-  const uint8_t *wp[4], *xp[kXLoads], *wsp, *xsp;
+  // Weights: bytes from the expert's first row (below 2^32), the expert's rows the same for all.
+  uint32_t wo[4], wso;
+  const uint8_t *w_base, *ws_base, *xp[kXLoads], *xsp;
   const int piece = ((lane & 7) ^ mx_swizzle(lane >> 3)) * 16, half = (lane & 1) * 4;
-  const int xs_row = 32 * (wave % (BM / 32)) + (lane >> 1);
+  const int xs_row = 32 * (wave % kXScaleLoads);
   // LDS row 16 r + m of a wavefront's weights holds MFMA row m of group r: columns 8 (m / 4) +
   // 4 r + m % 4 of its 32, so that a lane's two groups make eight consecutive columns; with SiTU
   // column m, the gate row in group 0 and the up row in group 1
   auto weight_row = [&](int i) {
     const int r = i >> 4, m = i & 15;
-    const int n = ld_cb * kCols + wave * (kCols / NW) + (SITU ? m : 8 * (m >> 2) + 4 * r + (m & 3));
-    return static_cast<int64_t>(ld.expert) * a.Nw + min(n, a.N - 1) + (SITU && r ? a.N : 0);
+    const int n = ld.cb * kCols + wave * (kCols / NW) + (SITU ? m : 8 * (m >> 2) + 4 * r + (m & 3));
+    return static_cast<uint32_t>(min(n, a.N - 1) + (SITU && r ? a.N : 0));
   };
-  // rows that are not there read the first of the tile; the epilogue leaves them out
-  auto token_row = [&](int i) {
-    const int64_t src = source_row(a, ld.row0 + (i < ld.nrows ? i : 0));
-    return src < 0 ? 0 : src;
-  };
-  auto begin_item = [&]() {
+  // An item's first half is done a chunk before it begins: which one it is, and (DIRECT) the loads
+  // of its row_idx, so that they are there by the second.
+  Item next;
+  bool more = true;
+  int idx[kXLoads + 1];
+  auto prepare = [&]() __attribute__((always_inline)) {
+    more = next_item(load_walk, &next);
+    if (!more || !DIRECT) return;
+    // rows that are not there read the first of the tile, and the epilogue leaves them out
+    auto row = [&](int i) { return a.row_idx[next.row0 + (i < next.nrows ? i : 0)]; };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) wp[j] = a.w + weight_row(8 * j + (lane >> 3)) * KB + piece;
-    wsp = a.w_mx + weight_row(lane >> 1) * SB + half;
-#pragma unroll
-    for (int j = 0; j < kXLoads; ++j)
-      xp[j] = a.x + token_row(8 * (NW * j + wave) + (lane >> 3)) * KB + piece;
-    xsp = a.x_mx + token_row(xs_row) * SB + half;
+    for (int j = 0; j < kXLoads; ++j) idx[j] = row(8 * (NW * j + wave) + (lane >> 3));
+    idx[kXLoads] = row(xs_row + (lane >> 1));
   };
-  auto load = [&](uint8_t* buf, int c) {
-    const int off = 128 * c, soff = 8 * c;
+  auto begin_item = [&]() __attribute__((always_inline)) {
+    if (!more) return;                                 // the last item again
+    ld = next;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wo[j] = weight_row(8 * j + (lane >> 3)) * KB + piece;
+    wso = weight_row(lane >> 1) * SB + half;
+    w_base = a.w + static_cast<int64_t>(ld.expert) * a.Nw * KB;
+    ws_base = a.w_mx + static_cast<int64_t>(ld.expert) * a.Nw * SB;
+    auto source = [&](int i, int j) -> int64_t {
+      if constexpr (DIRECT) return source_of(a, idx[j]);
+      const int row = ld.row0 + (i < ld.nrows ? i : 0);
+      return a.row_idx ? s_source[row] : row;
+    };
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j) {
+      const int64_t src = source(8 * (NW * j + wave) + (lane >> 3), j);
+      xp[j] = (src < 0 ? zeros : a.x + src * KB) + piece;
+    }
+    const int64_t src = source(xs_row + (lane >> 1), kXLoads);
+    xsp = (src < 0 ? zeros : a.x_mx + src * SB) + half;
+  };
+  // The load side's next chunk.  Behind the last item it loads that one again, so that the number
+  // of loads under way stays the same.
+  int lc = 0;
+  auto load = [&](uint8_t* buf) __attribute__((always_inline)) {
+    if (lc + 2 == nc) prepare();
+    const int off = 128 * lc, soff = 8 * lc;
     const bool in = off + piece < KB, s_in = soff + half < SB;
+    // (past the end of K the token rows are zeros, and the weights whatever the row begins with)
+    const uint32_t w_off = in ? off : 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      load_to_lds(in ? wp[j] + off : zero, buf + (32 * wave + 8 * j) * 128);
+      load_to_lds(w_base + (wo[j] + w_off), buf + (32 * wave + 8 * j) * 128);
 #pragma unroll
     for (int j = 0; j < kXLoads; ++j)
       load_to_lds(in ? xp[j] + off : zero, buf + (kRows + 8 * (NW * j + wave)) * 128);
-    load4_to_lds(s_in ? wsp + soff : zero, buf + kScales + 32 * wave * 8);
-    load4_to_lds(s_in ? xsp + soff : zero, buf + kScales + (kRows + 32 * (wave % (BM / 32))) * 8);
+    load4_to_lds(s_in ? ws_base + (wso + soff) : zero, buf + kScales + 32 * wave * 8);
+    load4_to_lds(s_in ? xsp + soff : zero, buf + kScales + (kRows + xs_row) * 8);
+    if (++lc == nc) {
+      lc = 0;
+      begin_item();
+    }
+  };
+  // this wavefront's loads of the chunk are in LDS, and it is done reading the buffers that the
+  // next loads write; after the barrier that holds for the workgroup
+  auto arrive = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_vm_lds((S - 2) * kLoads));
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  auto item = [&](auto mt_c, const TileRows tr, const int cb) {
-    constexpr int MT = decltype(mt_c)::value;
-    f32x4 acc[2][MT];
+  f32x4 acc[2][MT];
+  auto clear = [&]() {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[r][m] = f32x4{0, 0, 0, 0};
-    // this wavefront's loads of the chunk are in LDS, and it is done reading the buffers that
-    // the next loads write; after the barrier that holds for the workgroup
-    auto arrive = [&]() {
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(wait_vm_lds((S - 2) * kLoads));
-      asm volatile("s_barrier" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
+  };
+  auto compute = [&](const uint8_t* buf) __attribute__((always_inline)) {
+    auto fragment = [&](int row, int f) {
+      return *reinterpret_cast<const u32x4*>(buf + row * 128 + (((2 * g + f) ^ mx_swizzle(l16)) << 4));
     };
-    auto compute = [&](const uint8_t* buf) {
-      auto fragment = [&](int row, int f) {
-        return *reinterpret_cast<const u32x4*>(buf + row * 128 + (((2 * g + f) ^ mx_swizzle(l16)) << 4));
-      };
-      auto scales = [&](int row) -> uint32_t {
-        return *reinterpret_cast<const uint16_t*>(buf + kScales + row * 8 + 2 * g);
-      };
-      u32x4 wf[2][2];
-      uint32_t ws[2];
+    auto scales = [&](int row) -> uint32_t {
+      return *reinterpret_cast<const uint16_t*>(buf + kScales + row * 8 + 2 * g);
+    };
+    u32x4 wf[2][2];
+    uint32_t ws[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        ws[r] = scales(32 * wave + 16 * r + l16);
+    for (int r = 0; r < 2; ++r) {
+      ws[r] = scales(32 * wave + 16 * r + l16);
 #pragma unroll
-        for (int f = 0; f < 2; ++f) wf[r][f] = fragment(32 * wave + 16 * r + l16, f);
-      }
+      for (int f = 0; f < 2; ++f) wf[r][f] = fragment(32 * wave + 16 * r + l16, f);
+    }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < MT; ++m) {
+      if (m == 0 || 16 * m < it.nrows) {
         const int row = kRows + 16 * m + l16;
         const u32x4 x0 = fragment(row, 0), x1 = fragment(row, 1);
         const uint32_t xs = scales(row);
@@ -205,65 +413,78 @@ __global__ __launch_bounds__(NW * 64, NW * PER_CU / 4) void grouped_mx_mid_kerne
           acc[r][m] = mx_mma<0>(wf[r][0], x0, acc[r][m], ws[r], xs);
           acc[r][m] = mx_mma<1>(wf[r][1], x1, acc[r][m], ws[r], xs);
         }
-      }
-    };
-    for (int c = 0; c < nc; c += S) {
-      const bool last = c + S == nc;
-      for_ring<S>([&](auto u) {
-        constexpr int U = decltype(u)::value;
-        arrive();
-        // after an item's last chunk the first of the next item, or of this one again behind
-        // the last item, so that the number of loads under way stays the same
-        if constexpr (U == 1) {
-          if (last) {
-            more = walk.next<BM>(&ld, &ld_cb);
-            if (more) begin_item();
-          }
+        // (read all at once the fragments of eight groups spilled)
+        if constexpr (MT > 4) {
+          if (m % 2 == 1) __builtin_amdgcn_sched_barrier(0);
         }
-        load(ring(IntC<U + S - 1>{}), U > 0 && last ? U - 1 : c + U + S - 1);
-        compute(ring(u));
-      });
+      }
     }
-    constexpr int C = SITU ? 1 : 2;
-    Epilogue<0, SITU, C, MT> out(a);
-    const int n0 = cb * kCols + wave * (kCols / NW);
-    out.begin(tr.expert, [&](int n) { return n0 + (SITU ? 4 * g : 8 * g + 4 * n); },
-              [&](int m) { return 16 * m + l16 < tr.nrows ? tr.row0 + 16 * m + l16 : -1; });
+  };
+  auto epilogue = [&]() __attribute__((always_inline)) {
+    const int n = it.cb * kCols + wave * (kCols / NW) + (SITU ? 4 * g : 8 * g);
+    float beta = 0, ib = 0, lam = 0, il = 0;
+    if constexpr (SITU) {
+      beta = uniform(a.beta ? a.beta[it.expert] : 4.0f);
+      lam = uniform(a.lam ? a.lam[it.expert] : 25.0f);
+      ib = uniform(1.0f / beta);
+      il = uniform(1.0f / lam);
+    }
+    uint16_t* o = a.out + static_cast<int64_t>(it.row0 + l16) * a.N + n;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (out.row[m] < 0) continue;
-      if constexpr (SITU)
-        out.store(0, m, out.columns(0, m, acc[0][m], acc[1][m]));
-      else
-        out.store(0, m, out.columns(0, m, acc[0][m], acc[0][m]),
-                  out.columns(1, m, acc[1][m], acc[1][m]));
+      if (16 * m + l16 < it.nrows) {
+        if constexpr (SITU) {
+          float v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = situ_f32(acc[0][m][i], acc[1][m][i], beta, ib, lam, il);
+          store_columns(o, make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])), a.N, n);
+        } else {
+          const f32x4 c = acc[0][m], d = acc[1][m];
+          store_columns(o, u32x4{pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]),
+                                 pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3])}, a.N, n);
+        }
+      }
+      o += static_cast<int64_t>(16) * a.N;
     }
   };
 
+  prepare();
   begin_item();
-  TileRows tr = ld;
-  int cb = ld_cb;
-  // The load side is S - 1 chunks ahead: it is in the item that the other side begins.
-  for_ring<S - 1>([&](auto u) { load(ring(u), decltype(u)::value); });
-  for (;;) {
-    const int mt = (tr.nrows + 15) / 16;
-    if (mt <= 1) item(IntC<1>{}, tr, cb);
-    else if (mt <= 2) item(IntC<2>{}, tr, cb);
-    else if (BM == 64 || mt <= 4) item(IntC<BM >= 64 ? 4 : 2>{}, tr, cb);
-    else if (mt <= 6) item(IntC<BM >= 128 ? 6 : 2>{}, tr, cb);
-    else item(IntC<BM >= 128 ? 8 : 2>{}, tr, cb);
-    if (!more) break;
-    tr = ld;
-    cb = ld_cb;
+  for_ring<S - 1>([&](auto u) { load(ring(u)); });
+  clear();
+  // An item may end at any buffer of the ring.  The steps of a round are taken whatever happens in
+  // it, behind the last item on chunks that nobody stores: with a step left out on some path the
+  // compiler no longer knows how many loads are under way and waits for all of them.
+  int c = 0;
+  bool alive = true;
+  while (alive) {
+    for_ring<S>([&](auto u) __attribute__((always_inline)) {
+      arrive();
+      load(ring(IntC<decltype(u)::value + S - 1>{}));
+      compute(ring(u));
+      if (++c == nc) {
+        c = 0;
+        if (alive) {
+          epilogue();
+          clear();
+          alive = next_item(walk, &it);
+        }
+      }
+    });
   }
   __builtin_amdgcn_s_waitcnt(0);                       // no load into LDS outlives the workgroup
 }
 
 template <bool SITU, int BM, int NW, int PER_CU, int S>
 static hipError_t launch_mx_mid(const MxGroupedArgs& a, hipStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(a.cus / a.xcds * a.xcds * PER_CU);
-  grouped_mx_mid_kernel<SITU, BM, NW, PER_CU, S>
-      <<<dim3(grid), dim3(NW * 64), (static_cast<size_t>(a.E) + 1) * 4, stream>>>(a);
+  const dim3 grid(static_cast<unsigned>(a.cus / a.xcds * a.xcds * PER_CU)), block(NW * 64);
+  // the list has to fit behind the ring too (160 KB, less what the scan takes)
+  constexpr size_t kRing = S * ((32 * NW + BM) * 128 + (32 * NW + (BM < 32 ? 32 : BM)) * 8);
+  const size_t starts = (static_cast<size_t>(a.E) + 1) * 4, list = a.row_idx ? size_t(a.R) * 4 : 0;
+  const bool direct = a.row_idx && (a.R > kMxListRows || kRing + starts + list > 163840 - 128);
+  const size_t lds = starts + (direct ? 0 : list);
+  if (direct) grouped_mx_mid_kernel<SITU, true, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
+  else grouped_mx_mid_kernel<SITU, false, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -297,8 +518,8 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
   __shared__ alignas(16) uint8_t s_w0[kMxBufBytes], s_w1[kMxBufBytes], s_x0[kMxBufBytes],
       s_x1[kMxBufBytes];
   __shared__ alignas(16) u32x4 s_scale[2 * kMxTile];
-  scan_experts<kMxWaves>(a, s_tile, a.R / kMxTile, [](int n) { return n / kMxTile; });
-  scan_experts<kMxWaves>(a, s_tile + a.E + 1, 2 * min(a.R, a.E), [](int n) {
+  mx_scan<kMxWaves>(a, s_tile, a.R / kMxTile, [](int n) { return n / kMxTile; });
+  mx_scan<kMxWaves>(a, s_tile + a.E + 1, 2 * min(a.R, a.E), [](int n) {
     return (n % kMxTile + kMxTile / 2 - 1) / (kMxTile / 2);
   });
   constexpr int kCols = kMxTile / (SITU ? 2 : 1);
@@ -616,19 +837,38 @@ static hipError_t launch_mx_big(const MxGroupedArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Which kernel.  Larger tiles read the weights for more rows at once; smaller ones and smaller
+// blocks of weight rows make more work items.  items() is an upper bound of the items of a kernel
+// (the host does not know the rows of each expert), `few` three quarters of the CUs.  Measured on
+// one MI355X, us with tiles of 256 / 128 / 64 rows by 256 weight rows, 64 by 128, 32 by 64 and 16
+// by 64:
+//   many rows per expert: 64 experts x 512 rows, N = K = 2048  130 / 146 / 190 / 183 / 287 / 438;
+//     x 256 rows (half of the experts above one tile)  80 / 84 / 103 / 100 / 157 / 230, but 896 x
+//     292 rows, N = 384 with SiTU, K = 3584  986 / 872 / 1138 / 1373 / 2282 / 2614; 8 x 256 rows,
+//     N = K = 4096, whose tiles of 256 are one round of the chip  43 / 55 / 58 / 52 / 76 / 109;
+//   fewer: 896 x 73 rows, the same N and K  440 / 347 / 458 / 522 / 707 / 798; 18 rows, N = 3584,
+//     K = 384, Zipf  345 / 216 / 210 / 284 / 321 / 251; 4.6 rows  288 / 202 / 186 / 240 / 237 / 158;
+//     1.1 rows, N = 384 with SiTU, K = 3584  112 / 77 / 76 / 85 / 83 / 72;
+//   few items: 8 experts x 32 rows, N = K = 4096  26 / 24 / 24 / 18 / 24 / 28; one expert, N = K =
+//     7168, 512 rows  52 / 46 / 36 / 36 / 52 / 81, 64 rows  34 / 34 / 33 / 21 / 15 / 17, 16 rows
+//     33 / 29 / 28 / 18 / 13 / 13.
 template <bool SITU>
 static hipError_t launch_mx_one(const MxGroupedArgs& a, hipStream_t stream) {
-  const int64_t R = a.R, E = a.E, few = a.cus * 3 / 4;
-  auto items = [&](int tile, int block) {
-    return (std::min(R, E) + R / tile) * ((a.Nw + block - 1) / block);
-  };
-  if (E <= 1024 && R >= 448 * E && items(256, 256) >= few) return launch_mx_big<SITU>(a, stream);
-  const int64_t items128 = items(128, 256);
-  if (E <= 1536 && (items128 >= 8 * a.cus || (R > 40 * E && items128 >= few)))
-    return launch_mx_mid<SITU, 128, 8, 1, 3>(a, stream);
-  if (R > 24 * E && items(64, 128) >= few) return launch_mx_mid<SITU, 64, 4, 2, 3>(a, stream);
-  if (a.KB >= 1024) return launch_mx_mid<SITU, 32, 2, 2, 6>(a, stream);
-  return launch_mx_mid<SITU, 32, 4, 2, 3>(a, stream);
+  const int64_t R = a.R, E = a.E, some = std::min(R, E), few = a.cus * 3 / 4;
+  auto items = [&](int tile, int block) { return (some + R / tile) * ((a.Nw + block - 1) / block); };
+  // (the LDS of the larger tiles leaves room for so many experts' prefix sums)
+  const int64_t items256 = items(256, 256);
+  if (E <= 1024 && items256 >= few && (R >= 448 * E || (R >= 224 * E && items256 <= a.cus)))
+    return launch_mx_big<SITU>(a, stream);
+  if (items(128, 256) >= few) {
+    if (E <= 1536 && R > 32 * E) return launch_mx_mid<SITU, 128, 8, 1, 3>(a, stream);
+    if (E <= 8192 && R > 8 * E) return launch_mx_mid<SITU, 64, 8, 1, 3>(a, stream);
+    if (R > 8 * E) return launch_mx_mid<SITU, 64, 4, 2, 3>(a, stream);
+  } else if (R > 16 * some) {
+    if (items(64, 128) >= few) return launch_mx_mid<SITU, 64, 4, 2, 3>(a, stream);
+    return launch_mx_mid<SITU, 32, 2, 4, 3>(a, stream);
+  }
+  return launch_mx_mid<SITU, 16, 2, 4, 3>(a, stream);
 }
 
 hipError_t launch_grouped_mxfp4(const MxGroupedArgs& a, hipStream_t stream) {
