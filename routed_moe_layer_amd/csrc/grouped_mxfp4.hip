@@ -96,6 +96,26 @@ __device__ __forceinline__ void ready() { asm volatile("s_nop 1" ::: "memory"); 
 // after 7 wait states, and code behind the loop may read it at once.
 __device__ __forceinline__ void settle() { asm volatile("s_nop 7" ::: "memory"); }
 
+// Where loads into LDS read an operand.  Loads through a buffer descriptor take a 32-bit offset
+// per lane and one for all lanes, and give zeros for an offset past its end (kNowhere): a load is
+// one instruction behind the one that says where in LDS, its lanes' ends of K one more.  With
+// addresses of 64 bits (WIDE, for operands of 4 GB and more: a workgroup's weights are one
+// expert's, and its token rows those of a tile where nothing gathers them) it is three or four more,
+// and a chunk's loads were most of what a wavefront did.
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+constexpr uint32_t kNowhere = 0xFFFF0000u, kBufferMost = kNowhere;
+__device__ __forceinline__ buffer_t mx_buffer(const uint8_t* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(bytes),
+                                           0x00020000);
+}
+template <int BYTES>
+__device__ __forceinline__ void mx_load(buffer_t from, uint32_t lane_off, int off, uint8_t* to) {
+  if constexpr (BYTES == 16)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)to, 16, static_cast<int>(lane_off), off, 0, 0);
+  else
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)to, 4, static_cast<int>(lane_off), off, 0, 0);
+}
+
 // The last i with s[i] <= v, for rising s[0 .. n] with s[0] <= v < s[n], n <= 2^18: 64 entries at a
 // time are looked at by the lanes, so that a search is two or three LDS reads long.
 __device__ __forceinline__ int mx_last_at_most(const int32_t* s, int n, int v) {
@@ -232,8 +252,8 @@ struct MxItemWalk {
 // it wait for more).
 //
 // Bound by the bytes: FC1 of 16 tokens over 896 experts (N = 384 with SiTU, K = 3584, 328 MB) 71
-// us, 4.6 TB/s; FC1 of 4096 tokens (1.37 GB) 345 us, 4.0 TB/s; FC2 of 1024 Zipf tokens (N = 3584,
-// K = 384, 763 MB) 209 us, 3.6 TB/s, two chunks an item, half of the second of them zeros; a large
+// us, 4.6 TB/s; FC1 of 4096 tokens (1.37 GB) 331 us, 4.1 TB/s; FC2 of 1024 Zipf tokens (N = 3584,
+// K = 384, 763 MB) 207 us, 3.7 TB/s, two chunks an item, half of the second of them zeros; a large
 // read on the same card 5.99 TB/s.  A CU takes in about 20 bytes a ns this way, whether they come
 // from memory or from a cache, and the token rows' count with the weights'.  Eight wavefronts per
 // CU are needed for that: longer rings with four took 76 to 101 us for the 71.
@@ -244,7 +264,7 @@ struct MxItemWalk {
 // kMxListRows, in a list in LDS.
 constexpr int kMxListRows = 2048;
 
-template <bool SITU, bool DIRECT, int BM, int NW, int PER_CU, int S>
+template <bool SITU, bool DIRECT, bool WIDE, int BM, int NW, int PER_CU, int S>
 __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid_kernel(MxGroupedArgs a) {
   constexpr int kRows = 32 * NW, kCols = kRows / (SITU ? 2 : 1), MT = BM / 16;
   constexpr int kXLoads = BM / (8 * NW), kLoads = 6 + kXLoads;       // per wavefront and chunk
@@ -288,7 +308,7 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
       const int cnt = r.y - r.x, nt = (cnt + BM - 1) / BM;
       const int per = nt == 1 ? BM : ((cnt + nt - 1) / nt + 15) / 16 * 16;
       it->expert = e;
-      it->row0 = r.x + (tile - s_tile[e]) * per;
+      it->row0 = __builtin_amdgcn_readfirstlane(r.x + (tile - s_tile[e]) * per);
       it->nrows = min(per, r.y - it->row0);
       if (it->nrows > 0) return true;
     }
@@ -301,9 +321,11 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
   // Load j of a wavefront fills rows 8 j + lane / 8 of its 32 weight rows, or of its token rows,
   // slot lane % 8 of a row with piece (lane % 8) ^ mx_swizzle(row).  A load of scales takes 32
   // rows, two lanes each.
-  // Weights: bytes from the expert's first row (below 2^32), the expert's rows the same for all.
-  uint32_t wo[4], wso;
-  const uint8_t *w_base, *ws_base, *xp[kXLoads], *xsp;
+  // Offsets from the expert's first weights, and from all token rows or (nothing gathers them) the
+  // tile's first; WIDE: addresses.
+  uint32_t wo[4], wso, xo[kXLoads], xso;
+  buffer_t w_buf, ws_buf, x_buf, xs_buf;
+  const uint8_t *wp[4], *wsp, *xp[kXLoads], *xsp;
   const int piece = ((lane & 7) ^ mx_swizzle(lane >> 3)) * 16, half = (lane & 1) * 4;
   const int xs_row = 32 * (wave % kXScaleLoads);
   // LDS row 16 r + m of a wavefront's weights holds MFMA row m of group r: columns 8 (m / 4) +
@@ -331,23 +353,42 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
   auto begin_item = [&]() __attribute__((always_inline)) {
     if (!more) return;                                 // the last item again
     ld = next;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) wo[j] = weight_row(8 * j + (lane >> 3)) * KB + piece;
-    wso = weight_row(lane >> 1) * SB + half;
-    w_base = a.w + static_cast<int64_t>(ld.expert) * a.Nw * KB;
-    ws_base = a.w_mx + static_cast<int64_t>(ld.expert) * a.Nw * SB;
+    const int64_t w_at = static_cast<int64_t>(ld.expert) * a.Nw;
+    const uint8_t *w = a.w + w_at * KB, *ws = a.w_mx + w_at * SB;
     auto source = [&](int i, int j) -> int64_t {
       if constexpr (DIRECT) return source_of(a, idx[j]);
       const int row = ld.row0 + (i < ld.nrows ? i : 0);
       return a.row_idx ? s_source[row] : row;
     };
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int j = 0; j < kXLoads; ++j) {
-      const int64_t src = source(8 * (NW * j + wave) + (lane >> 3), j);
-      xp[j] = (src < 0 ? zeros : a.x + src * KB) + piece;
+      for (int j = 0; j < 4; ++j) wp[j] = w + static_cast<int64_t>(weight_row(8 * j + (lane >> 3))) * KB + piece;
+      wsp = ws + static_cast<int64_t>(weight_row(lane >> 1)) * SB + half;
+#pragma unroll
+      for (int j = 0; j < kXLoads; ++j) {
+        const int64_t src = source(8 * (NW * j + wave) + (lane >> 3), j);
+        xp[j] = (src < 0 ? zeros : a.x + src * KB) + piece;
+      }
+      const int64_t src = source(xs_row + (lane >> 1), kXLoads);
+      xsp = (src < 0 ? zeros : a.x_mx + src * SB) + half;
+    } else {
+      w_buf = mx_buffer(w, static_cast<uint32_t>(a.Nw) * KB);
+      ws_buf = mx_buffer(ws, static_cast<uint32_t>(a.Nw) * SB);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wo[j] = weight_row(8 * j + (lane >> 3)) * KB + piece;
+      wso = weight_row(lane >> 1) * SB + half;
+      const bool gathered = a.row_idx != nullptr;
+      const int first = gathered ? 0 : ld.row0, rows = gathered ? a.x_rows : ld.nrows;
+      x_buf = mx_buffer(a.x + static_cast<int64_t>(first) * KB, static_cast<uint32_t>(rows) * KB);
+      xs_buf = mx_buffer(a.x_mx + static_cast<int64_t>(first) * SB, static_cast<uint32_t>(rows) * SB);
+#pragma unroll
+      for (int j = 0; j < kXLoads; ++j) {
+        const int src = static_cast<int>(source(8 * (NW * j + wave) + (lane >> 3), j));
+        xo[j] = src < 0 ? kNowhere : static_cast<uint32_t>(src - first) * KB + piece;
+      }
+      const int src = static_cast<int>(source(xs_row + (lane >> 1), kXLoads));
+      xso = src < 0 ? kNowhere : static_cast<uint32_t>(src - first) * SB + half;
     }
-    const int64_t src = source(xs_row + (lane >> 1), kXLoads);
-    xsp = (src < 0 ? zeros : a.x_mx + src * SB) + half;
   };
   // The load side's next chunk.  Behind the last item it loads that one again, so that the number
   // of loads under way stays the same.
@@ -356,16 +397,24 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
     if (lc + 2 == nc) prepare();
     const int off = 128 * lc, soff = 8 * lc;
     const bool in = off + piece < KB, s_in = soff + half < SB;
-    // (past the end of K the token rows are zeros, and the weights whatever the row begins with)
-    const uint32_t w_off = in ? off : 0;
+    auto to = [&](int j) { return buf + (32 * wave + 8 * j) * 128; };
+    auto x_to = [&](int j) { return buf + (kRows + 8 * (NW * j + wave)) * 128; };
+    uint8_t *ws_to = buf + kScales + 32 * wave * 8, *xs_to = buf + kScales + (kRows + xs_row) * 8;
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      load_to_lds(w_base + (wo[j] + w_off), buf + (32 * wave + 8 * j) * 128);
+      for (int j = 0; j < 4; ++j) load_to_lds(in ? wp[j] + off : zero, to(j));
 #pragma unroll
-    for (int j = 0; j < kXLoads; ++j)
-      load_to_lds(in ? xp[j] + off : zero, buf + (kRows + 8 * (NW * j + wave)) * 128);
-    load4_to_lds(s_in ? ws_base + (wso + soff) : zero, buf + kScales + 32 * wave * 8);
-    load4_to_lds(s_in ? xsp + soff : zero, buf + kScales + (kRows + xs_row) * 8);
+      for (int j = 0; j < kXLoads; ++j) load_to_lds(in ? xp[j] + off : zero, x_to(j));
+      load4_to_lds(s_in ? wsp + soff : zero, ws_to);
+      load4_to_lds(s_in ? xsp + soff : zero, xs_to);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx_load<16>(w_buf, in ? wo[j] : kNowhere, off, to(j));
+#pragma unroll
+      for (int j = 0; j < kXLoads; ++j) mx_load<16>(x_buf, in ? xo[j] : kNowhere, off, x_to(j));
+      mx_load<4>(ws_buf, s_in ? wso : kNowhere, soff, ws_to);
+      mx_load<4>(xs_buf, s_in ? xso : kNowhere, soff, xs_to);
+    }
     if (++lc == nc) {
       lc = 0;
       begin_item();
@@ -475,16 +524,27 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
   __builtin_amdgcn_s_waitcnt(0);                       // no load into LDS outlives the workgroup
 }
 
+static bool mx_wide(const MxGroupedArgs& a) {
+  return static_cast<uint64_t>(a.Nw) * a.KB > kBufferMost ||
+         (a.row_idx && static_cast<uint64_t>(a.x_rows) * a.KB > kBufferMost);
+}
+
 template <bool SITU, int BM, int NW, int PER_CU, int S>
 static hipError_t launch_mx_mid(const MxGroupedArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.cus / a.xcds * a.xcds * PER_CU)), block(NW * 64);
   // the list has to fit behind the ring too (160 KB, less what the scan takes)
   constexpr size_t kRing = S * ((32 * NW + BM) * 128 + (32 * NW + (BM < 32 ? 32 : BM)) * 8);
   const size_t starts = (static_cast<size_t>(a.E) + 1) * 4, list = a.row_idx ? size_t(a.R) * 4 : 0;
-  const bool direct = a.row_idx && (a.R > kMxListRows || kRing + starts + list > 163840 - 128);
+  const bool direct = a.row_idx && (a.R > kMxListRows || kRing + starts + list > 163840 - 128 || mx_wide(a));
   const size_t lds = starts + (direct ? 0 : list);
-  if (direct) grouped_mx_mid_kernel<SITU, true, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
-  else grouped_mx_mid_kernel<SITU, false, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
+  if (mx_wide(a)) {
+    if (direct) grouped_mx_mid_kernel<SITU, true, true, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
+    else grouped_mx_mid_kernel<SITU, false, true, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
+  } else if (direct) {
+    grouped_mx_mid_kernel<SITU, true, false, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
+  } else {
+    grouped_mx_mid_kernel<SITU, false, false, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
+  }
   return hipGetLastError();
 }
 
@@ -503,16 +563,16 @@ static hipError_t launch_mx_mid(const MxGroupedArgs& a, hipStream_t stream) {
 // selector of the instruction.
 //
 // Bound by the matrix units, the LDS and the caches together and by the power they draw: 8192^3
-// takes 251 us, 4.4 PFLOP/s (the instruction alone on random codes 6.7, with the clock down to
-// 1.6 GHz; the same kernel without its loads 4.6, without its LDS reads 4.7; the library's product
-// 2.9).  8 experts x 4096 rows (N = 3584, K = 4096) take 276 us, 3.5 PFLOP/s, in seven to eight
-// rounds of items.  Eight wavefronts of 128 x 64 products read 1.5 times as much from LDS.
+// takes 241 us, 4.6 PFLOP/s (the instruction alone on random codes 6.7, with the clock down to
+// 1.6 GHz; an earlier state at 4.0 made 4.6 without its loads and 4.7 without its LDS reads; the
+// library's product 2.9).  8 experts x 4096 rows (N = 3584, K = 4096) take 267 us, 3.6 PFLOP/s, in
+// seven to eight rounds of items.  Eight wavefronts of 128 x 64 products read 1.5 times as much from LDS.
 // ---------------------------------------------------------------------------------------
 constexpr int kWaitLds = 0xC07F;                       // s_waitcnt for LDS reads alone
 constexpr int kMxTile = 256, kMxWaves = 4, kMxThreads = kMxWaves * 64;
 constexpr int kMxBufBytes = kMxTile * 128, kMxBufLoads = kMxBufBytes / 1024 / kMxWaves;
 
-template <bool SITU>
+template <bool SITU, bool WIDE>
 __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGroupedArgs a) {
   extern __shared__ int32_t s_tile[];                  // two prefix sums of E + 1
   __shared__ alignas(16) uint8_t s_w0[kMxBufBytes], s_w1[kMxBufBytes], s_x0[kMxBufBytes],
@@ -546,39 +606,60 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
     int n;
     if (SITU) n = ld_cb * kCols + 64 * q + 32 * (r >> 2) + 8 * (m >> 2) + 4 * ((r >> 1) & 1) + (m & 3);
     else n = ld_cb * kCols + 128 * q + 32 * (r >> 1) + 8 * (m >> 2) + 4 * (r & 1) + (m & 3);
-    return static_cast<int64_t>(ld.expert) * a.Nw + min(n, a.N - 1) + (SITU && (r & 1) ? a.N : 0);
+    return min(n, a.N - 1) + (SITU && (r & 1) ? a.N : 0);
   };
   // source row of token row i, -1 for zeros; rows that are not there read the first of the tile,
   // and the epilogue leaves them out
   auto token_row = [&](int i) { return source_row(a, ld.row0 + (i < ld.nrows ? i : 0)); };
   // Load j of a wave fills rows 64 wave + 8 j + lane / 8 of an operand, slot lane % 8 of a row
   // with piece (lane % 8) ^ mx_swizzle(row).  Thread t loads the scales of row t of both operands.
+  // Offsets (WIDE: addresses) as in the kernel above.
+  uint32_t wo[8], xo[8];
+  buffer_t w_buf, x_buf;
   const uint8_t *wp[8], *xp[8], *wsp, *xsp;
   const int piece = ((lane & 7) ^ mx_swizzle(lane >> 3)) * 16;
-  auto begin_item = [&]() {
+  auto begin_item = [&]() __attribute__((always_inline)) {
+    const int64_t w_at = static_cast<int64_t>(ld.expert) * a.Nw;
+    const uint8_t* w = a.w + w_at * KB;
+    const bool gathered = a.row_idx != nullptr;
+    const int first = gathered ? 0 : __builtin_amdgcn_readfirstlane(ld.row0);
+    const int rows = gathered ? a.x_rows : __builtin_amdgcn_readfirstlane(ld.nrows);
+    w_buf = mx_buffer(w, static_cast<uint32_t>(a.Nw) * KB);
+    x_buf = mx_buffer(a.x + static_cast<int64_t>(first) * KB, static_cast<uint32_t>(rows) * KB);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int row = 64 * wave + 8 * j + (lane >> 3);
-      wp[j] = a.w + weight_row(row) * KB + piece;
       const int64_t src = token_row(row);
-      xp[j] = (src < 0 ? zeros : a.x + src * KB) + piece;
+      if constexpr (WIDE) {
+        wp[j] = w + static_cast<int64_t>(weight_row(row)) * KB + piece;
+        xp[j] = (src < 0 ? zeros : a.x + src * KB) + piece;
+      } else {
+        wo[j] = static_cast<uint32_t>(weight_row(row)) * KB + piece;
+        xo[j] = src < 0 ? kNowhere : static_cast<uint32_t>(static_cast<int>(src) - first) * KB + piece;
+      }
     }
     const int64_t src = token_row(tid);
-    wsp = a.w_mx + weight_row(tid) * SB;
+    wsp = a.w_mx + (w_at + weight_row(tid)) * SB;
     xsp = src < 0 ? zeros : a.x_mx + src * SB;
   };
-  auto source = [&](const uint8_t* (&p)[8], int c, int j) {
-    return 128 * c + piece < KB ? p[j] + 128 * c : zero;
+  // load j of chunk c of the weights or the token rows: where from (source), and the load
+  auto source = [&](auto weights, int c, int j) {
+    const bool in = 128 * c + piece < KB;
+    if constexpr (WIDE) return in ? (weights.value ? wp[j] : xp[j]) + 128 * c : zero;
+    else return in ? (weights.value ? wo[j] : xo[j]) : kNowhere;
   };
-  auto load = [&](const uint8_t* from, uint8_t* buf, int j) {
-    load_to_lds(from, buf + (64 * wave + 8 * j) * 128);
+  auto load = [&](auto weights, auto from, int c, uint8_t* buf, int j) {
+    uint8_t* to = buf + (64 * wave + 8 * j) * 128;
+    if constexpr (WIDE) load_to_lds(from, to);
+    else if constexpr (weights.value) mx_load<16>(w_buf, from, 128 * c, to);
+    else mx_load<16>(x_buf, from, 128 * c, to);
   };
   u32x4 sc[2];                                         // this thread's rows' scales of a round
   // (one load of 16 bytes, which needs no more than the dword's alignment: four of a dword each
   // are four requests for the line)
   // (loads from global memory in so many words: as flat ones they would not come back in order
   // with the loads into LDS, and those are counted)
-  auto load_scales = [&](int r) {
+  auto load_scales = [&](int r) __attribute__((always_inline)) {
     struct __attribute__((packed, aligned(4))) Piece { u32x4 v; };
     typedef const __attribute__((address_space(1))) Piece* PiecePtr;
     typedef const __attribute__((address_space(1))) uint32_t* WordPtr;
@@ -597,7 +678,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
     }
   };
   // dword g: bytes 2 g and 2 g + 1 of both chunks
-  auto write_scales = [&]() {
+  auto write_scales = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       const u32x4 v = sc[o];
@@ -609,7 +690,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
   };
   // the loads' next round: the item's next, or the first of the next item (of this one again
   // behind the last item, so that the number of loads under way stays the same)
-  auto advance = [&]() {
+  auto advance = [&]() __attribute__((always_inline)) {
     if (++ld_r == nr) {
       ld_r = 0;
       more = walk.next(&ld, &ld_cb);
@@ -618,7 +699,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
   };
 
   // One item whose rows fit 32 MG tokens; a wave has 16 MG of them.
-  auto item = [&](auto mg_c) {
+  auto item = [&](auto mg_c) __attribute__((always_inline)) {
     constexpr int MG = decltype(mg_c)::value;
     const int t0 = 16 * MG * wm;
     const TileRows tr = ld;
@@ -649,7 +730,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
     auto tokens = [&](const uint8_t* buf, int f, int m) {
       return *reinterpret_cast<const u32x4*>(buf + x_at + at[f] + 2048 * m);
     };
-    auto arrive = [&](bool wait) {
+    auto arrive = [&](bool wait) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
       if (wait) __builtin_amdgcn_s_waitcnt(wait_vm_lds(kMxBufLoads));
       else __builtin_amdgcn_s_waitcnt(kWaitLds);
@@ -657,7 +738,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
       __builtin_amdgcn_sched_barrier(0);
     };
     // batch q of a chunk (step q / NB), side(k) between its products k and k + 1
-    auto products = [&](auto uc, auto qc, auto side) {
+    auto products = [&](auto uc, auto qc, auto side) __attribute__((always_inline)) {
       constexpr int U = decltype(uc)::value, Q = decltype(qc)::value, m0 = Q % NB * BG;
       ready();
       for_ring<8 * BG>([&](auto kc) {
@@ -705,12 +786,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
           write_scales();
         }
         // load j of this step: its source, and the load
-        auto from = [&](int j) {
-          if constexpr (U == 0) return source(xp, 2 * ld_r + 1, j);
-          else if constexpr (U == 1) return source(wp, 2 * ld_r, j);
-          else if constexpr (U == 2) return source(xp, 2 * ld_r, j);
-          else return source(wp, 2 * ld_r + 1, j);
-        };
+        const IntC<U == 1 || U == 3> which;
+        const int lc = 2 * ld_r + (U == 0 || U == 3);
+        auto from = [&](int j) { return source(which, lc, j); };
         uint8_t* to = U == 0 ? s_x1 : U == 1 ? s_w0 : U == 2 ? s_x0 : s_w1;
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (F == 0) products(IntC<(U + 3) & 3>{}, IntC<2 * NB - 1>{}, nothing);
@@ -727,7 +805,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
             constexpr int w0 = 8 * B / kBatches, nw = 8 * (B + 1) / kBatches - w0;
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(kWaitLds);
-            const uint8_t* src = nullptr;
+            decltype(from(0)) src{};
             // behind product k: the next batch's token rows, the next step's weights, and this
             // batch's share of the loads, each with its source one product earlier
             products(uc, IntC<Q>{}, [&](auto kc) {
@@ -740,7 +818,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
                 } else if (i < BG + nw + 2 * nw) {
                   const int j = (i - BG - nw) / 2;
                   if ((i - BG - nw) % 2 == 0) src = from(w0 + j);
-                  else load(src, to, w0 + j);
+                  else load(which, src, lc, to, w0 + j);
                 }
               };
               side(k);
@@ -754,7 +832,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
 #pragma unroll
           for (int w = 0; w < 8; ++w) wf[0][w] = weights(w_next, 0, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) load(from(j), to, j);
+          for (int j = 0; j < 8; ++j) load(which, from(j), lc, to, j);
         }
       });
       settle();
@@ -771,7 +849,7 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
     const float lam = SITU ? uniform(a.lam ? a.lam[tr.expert] : 25.0f) : 0.0f;
     const float ib = SITU ? uniform(1.0f / beta) : 0.0f, il = SITU ? uniform(1.0f / lam) : 0.0f;
     // eight consecutive columns of token group m
-    auto columns = [&](int s, int m) {
+    auto columns = [&](int s, int m) __attribute__((always_inline)) {
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -788,34 +866,28 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
     constexpr int kSpans = SITU ? 2 : 4;               // of 32 columns, eight per lane
     const int n0 = cb * kCols + kCols / 2 * wn + 8 * g, rows = tr.nrows - t0 - l16;
     uint16_t* o = a.out + static_cast<int64_t>(tr.row0 + t0 + l16) * a.N + n0;
-    if (a.N % 8 == 0 && cb * kCols + kCols <= a.N) {
-#pragma unroll
-      for (int m = 0; m < MG; ++m) {
-        if (16 * m < rows) {
-#pragma unroll
-          for (int s = 0; s < kSpans; ++s) *reinterpret_cast<u32x4*>(o + 32 * s) = columns(s, m);
-        }
-        o += static_cast<int64_t>(16) * a.N;
+    const bool whole = a.N % 8 == 0 && cb * kCols + kCols <= a.N;
+    for_ring<MG>([&](auto mc) __attribute__((always_inline)) {
+      constexpr int m = decltype(mc)::value;
+      if (16 * m < rows) {
+        for_ring<kSpans>([&](auto sc) __attribute__((always_inline)) {
+          constexpr int s = decltype(sc)::value;
+          const u32x4 v = columns(s, m);
+          if (whole) *reinterpret_cast<u32x4*>(o + 32 * s) = v;
+          else store_columns(o + 32 * s, v, a.N, n0 + 32 * s);
+        });
       }
-    } else {
-#pragma unroll
-      for (int m = 0; m < MG; ++m) {
-        if (16 * m < rows) {
-#pragma unroll
-          for (int s = 0; s < kSpans; ++s) store_columns(o + 32 * s, columns(s, m), a.N, n0 + 32 * s);
-        }
-        o += static_cast<int64_t>(16) * a.N;
-      }
-    }
+      o += static_cast<int64_t>(16) * a.N;
+    });
   };
 
   begin_item();
   load_scales(0);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    load(source(wp, 0, j), s_w0, j);
-    load(source(xp, 0, j), s_x0, j);
-    load(source(wp, 1, j), s_w1, j);
+    load(IntC<1>{}, source(IntC<1>{}, 0, j), 0, s_w0, j);
+    load(IntC<0>{}, source(IntC<0>{}, 0, j), 0, s_x0, j);
+    load(IntC<1>{}, source(IntC<1>{}, 1, j), 1, s_w1, j);
   }
   write_scales();
   __builtin_amdgcn_s_waitcnt(0);
@@ -832,8 +904,9 @@ __global__ __launch_bounds__(kMxThreads, 1) void grouped_mx_big_kernel(MxGrouped
 template <bool SITU>
 static hipError_t launch_mx_big(const MxGroupedArgs& a, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(a.cus / a.xcds * a.xcds);
-  grouped_mx_big_kernel<SITU><<<dim3(grid), dim3(kMxThreads),
-                                (static_cast<size_t>(a.E) + 1) * 8, stream>>>(a);
+  const size_t lds = (static_cast<size_t>(a.E) + 1) * 8;
+  if (mx_wide(a)) grouped_mx_big_kernel<SITU, true><<<dim3(grid), dim3(kMxThreads), lds, stream>>>(a);
+  else grouped_mx_big_kernel<SITU, false><<<dim3(grid), dim3(kMxThreads), lds, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -364,6 +364,55 @@ def test_grouped_weights_and_outputs_past_32_bit_offsets():
         assert bool(((out[rows].double() - want).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("R,N,situ", [(5, 100, False), (40, 700, True), (300, 9000, False),
+                                      (2100, 1500, True), (4096, 3600, False), (4200, 1900, True)])
+def test_grouped_token_rows_past_32_bit_offsets(R, N, situ):
+    """Gathered rows of more than 4 GB of codes, on every tile size; some of them missing."""
+    _say(f"mxfp4 grouped wide rows R={R} N={N} situ={situ}")
+    K, x_rows = 16384, 530000                          # 4.3e9 bytes of codes
+    g = _gen(R)
+    x = torch.zeros((x_rows, K // 2), dtype=U8, device="cuda")
+    xs = torch.zeros((x_rows, K // 32), dtype=U8, device="cuda")
+    idx = torch.randint(0, x_rows, (R,), generator=g, device="cuda")
+    idx[-1], idx[R // 2] = x_rows - 1, x_rows - 2
+    p = _problem(R, 1, N, K, situ, False)
+    x[idx], xs[idx] = p["x"], p["xs"]
+    sub = dict(p, x=x[idx], xs=xs[idx])               # (where two rows share a source: what it holds)
+    gone = torch.zeros(R, dtype=torch.bool, device="cuda")
+    gone[1] = True
+    sub["row_idx"] = torch.where(gone, -1, torch.arange(R, device="cuda")).to(I32)
+    out, guard = _guarded(R, N)
+    idx = torch.where(gone, -1, idx).to(I32)
+    _call(dict(p, x=x, xs=xs, x_rows=x_rows, row_idx=idx), out)
+    torch.cuda.synchronize()
+    assert _intact(guard) and not bool(out[1].any())
+    _check(sub, out)
+
+
+@pytest.mark.parametrize("R", [3, 200])
+def test_grouped_weights_of_one_expert_past_32_bit_offsets(R):
+    _say(f"mxfp4 grouped wide weights R={R}")
+    N, K = 65536, 65536                                # 4.3e9 bytes of codes with SiTU
+    g = _gen(R)
+    x, xs = _random_rows(g, R, K, -6)
+    w, ws = torch.zeros((2 * N, K // 2), dtype=U8, device="cuda"), torch.full((2 * N, K // 32), 127, dtype=U8, device="cuda")
+    cols = torch.tensor([0, 1, 777, N - 2, N - 1], device="cuda")
+    rows = torch.cat((cols, cols + N))
+    w[rows], ws[rows] = _random_rows(g, rows.numel(), K, -6)
+    out, guard = _guarded(R, N)
+    cum = torch.tensor([R], dtype=I32, device="cuda")
+    beta, lam = torch.full((1,), 4.0), torch.full((1,), 25.0)
+    rm.moe_grouped_gemm_mxfp4(R, N, K, 1, x, xs, cum, w, ws, out, situ=True)
+    torch.cuda.synchronize()
+    assert _intact(guard)
+    want, tol, _ = ref.grouped(ref.decode(x, xs), torch.arange(R, device="cuda"), cum,
+                               lambda e: ref.decode(w[rows], ws[rows]), cols.numel(), beta, lam, True)
+    assert bool(((out[:, cols].double() - want).abs() <= tol).all())
+    others = torch.ones(N, dtype=torch.bool, device="cuda")
+    others[cols] = False
+    assert not bool(out[:, others].any())
+
+
 # one problem for each tile size and ring that the launch rule chooses between
 KERNELS = [(40, 1, 1100, 4128), (40, 4, 300, 544), (600, 1, 5000, 544), (9000, 16, 3000, 288),
            (20000, 3, 2000, 800), (20000, 3, 2000, 2080), (1, 1, 900, 2048), (3000, 600, 512, 384)]
