@@ -997,7 +997,7 @@ static moe_status_t balance_dims(int32_t T, int32_t num_experts) {
 // The workspace of G parts of E experts; returns its bytes.
 static size_t balance_carve(int G, int E, uint8_t* base, BalanceArgs* a) {
   Carver c;
-  const size_t joins = (static_cast<size_t>(E) + 63) / 64;
+  const size_t joins = (static_cast<size_t>(E) + kBalanceJoinExperts - 1) / kBalanceJoinExperts;
   const size_t dot = c.take(joins * sizeof(double)), routed = c.take(joins * sizeof(int64_t));
   const size_t ticket = c.take(sizeof(uint32_t)), tokens = c.take(static_cast<size_t>(G) * 4);
   const size_t sums = c.take(static_cast<size_t>(G) * E * 4);

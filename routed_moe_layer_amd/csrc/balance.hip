@@ -7,15 +7,19 @@
 // the probabilities sum to one: nearly equal counts keep their differences, equal ones give 0.
 //
 // A row is held in registers by LPR lanes (4, 16 or 64 by the number of experts), V values each,
-// so it is read once; the next row's loads are under way meanwhile.  The sums over tokens stay
-// in the same lanes, then go over the workgroup's wavefronts in LDS and over the workgroups in
-// a second launch, each in a fixed order, so a call's result never depends on timing.
+// so it is read once; the next row's loads are under way meanwhile, and the mask of the one behind
+// it.  The sums over tokens stay in the same lanes, then go over the workgroup's wavefronts in LDS
+// and over the workgroups in a second launch, each in a fixed order, so a call's result never
+// depends on timing.
 #include "common.h"
 #include "kernels.h"
 
 namespace rmoe {
 
-constexpr int kBalanceWaves = 8;
+// Wavefronts of a workgroup, and rows of sums that they share in LDS: with more than 1024 experts a
+// row's registers leave room for half as many wavefronts, and LDS for fewer rows.
+constexpr int balance_waves(int V) { return V <= 16 ? 16 : 8; }
+constexpr int balance_slots(int V) { return V <= 16 ? 8 : 2; }
 
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ float dppf(float old, float x) {
@@ -65,7 +69,8 @@ __device__ __forceinline__ int expert_of(int sub, int v) {
 
 // A lane's V values of a row, `pad` past the last expert.  VEC needs E a multiple of 4 and rows
 // aligned to four values.
-template <bool BF16, int LPR, int V, bool VEC>
+// NT: past the caches.
+template <bool BF16, int LPR, int V, bool VEC, bool NT>
 __device__ __forceinline__ void load_row(const void* base, int64_t row, int E, int sub, float pad,
                                          float (&z)[V]) {
   if constexpr (VEC) {
@@ -74,14 +79,16 @@ __device__ __forceinline__ void load_row(const void* base, int64_t row, int E, i
       const int e = 4 * (sub + LPR * i);
       if (e < E) {
         if constexpr (BF16) {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + row * E + e);
+          const u32x2* p = reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(base) + row * E + e);
+          const u32x2 w = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             z[4 * i + 2 * j] = __uint_as_float(w[j] << 16);
             z[4 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
           }
         } else {
-          const f32x4 w = *reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + row * E + e);
+          const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + row * E + e);
+          const f32x4 w = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
           for (int j = 0; j < 4; ++j) z[4 * i + j] = w[j];
         }
@@ -123,52 +130,49 @@ __device__ __forceinline__ float softmax_parts(float (&z)[V]) {
 }
 
 template <bool BF16, int LPR, int V, bool VEC>
-__global__ __launch_bounds__(kBalanceWaves * 64, 2) void balance_stats_kernel(BalanceArgs a) {
-  constexpr int kRows = 64 / LPR;                      // rows per wavefront
+__global__ __launch_bounds__(balance_waves(V) * 64) void balance_stats_kernel(BalanceArgs a) {
+  constexpr int kRows = 64 / LPR, kWaves = balance_waves(V), kSlots = balance_slots(V);
+  constexpr int kThreads = kWaves * 64;
   extern __shared__ char s_raw[];
-  float* s_sum = reinterpret_cast<float*>(s_raw);
-  int32_t* s_count = reinterpret_cast<int32_t*>(s_raw) + a.E;
+  float* s_sum = reinterpret_cast<float*>(s_raw);      // [kSlots][E]
+  int32_t* s_count = reinterpret_cast<int32_t*>(s_raw) + kSlots * a.E;
   __shared__ int32_t s_tokens, s_routed;
-  __shared__ double s_dot[kBalanceWaves];
+  __shared__ double s_dot[kWaves];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, sub = lane % LPR;
-  constexpr int kThreads = kBalanceWaves * 64;
-  for (int e = tid; e < a.E; e += kThreads) {
-    s_sum[e] = 0.0f;
-    s_count[e] = 0;
-  }
-  if (tid == 0) s_tokens = s_routed = 0;
-  __syncthreads();
-
-  const int step = static_cast<int>(gridDim.x) * kBalanceWaves * kRows;
-  int t = (static_cast<int>(blockIdx.x) * kBalanceWaves + wave) * kRows + lane / LPR;
+  const int step = static_cast<int>(gridDim.x) * kWaves * kRows;
+  int t = (static_cast<int>(blockIdx.x) * kWaves + wave) * kRows + lane / LPR;
   float z[V], acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
   auto counted = [&](int row) { return row < a.T && (!a.mask || a.mask[row]); };
   // rows that do not count are never read
-  auto fetch = [&](int row, float (&to)[V]) {
-    if (counted(row)) {
-      load_row<BF16, LPR, V, VEC>(a.logits, row, a.E, sub, -__builtin_inff(), to);
+  auto fetch = [&](int row, bool live, float (&to)[V]) {
+    if (live) {
+      load_row<BF16, LPR, V, VEC, false>(a.logits, row, a.E, sub, -__builtin_inff(), to);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) to[v] = -__builtin_inff();
     }
   };
-  fetch(t, z);
+  bool live = counted(t + step);                       // of the row behind the one under way
+  fetch(t, counted(t), z);
+  for (int e = tid; e < a.E; e += kThreads) s_count[e] = 0;
+  if (tid == 0) s_tokens = s_routed = 0;
+  __syncthreads();
   // the experts' counts, while the first rows are on their way
   int tokens = 0;
   const int ids = a.T * a.k;
   for (int f = static_cast<int>(blockIdx.x) * kThreads + tid; f < ids; f += static_cast<int>(gridDim.x) * kThreads) {
-    const int row = f / a.k;
+    const int row = f / a.k, e = a.ids[f];
     if (!counted(row)) continue;
     if (f == row * a.k) ++tokens;
-    const int e = a.ids[f];
     if (e >= 0 && e < a.E) atomicAdd(&s_count[e], 1);
   }
   if (tokens) atomicAdd(&s_tokens, tokens);
   for (int base = t - lane / LPR; base < a.T; base += step, t += step) {   // whole wavefronts
     float next[V];
-    fetch(t + step, next);
+    fetch(t + step, live, next);
+    live = counted(t + 2 * step);
     const float inv = softmax_parts<LPR, V>(z);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -183,15 +187,23 @@ __global__ __launch_bounds__(kBalanceWaves * 64, 2) void balance_stats_kernel(Ba
       for (int off = LPR; off < 64; off <<= 1) acc[v] += __shfl_xor(acc[v], off);
     }
   }
-  for (int w = 0; w < kBalanceWaves; ++w) {
-    if (wave == w && lane < LPR) {
+#pragma unroll
+  for (int w = 0; w < kWaves; w += kSlots) {
+    if (wave / kSlots == w / kSlots && lane < LPR) {
+      float* to = s_sum + (wave % kSlots) * a.E;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int e = expert_of<LPR, VEC>(sub, v);
-        if (e < a.E) s_sum[e] += acc[v];
+        if (e < a.E) to[e] = w == 0 ? acc[v] : to[e] + acc[v];
       }
     }
     __syncthreads();
+  }
+  for (int e = tid; e < a.E; e += kThreads) {          // (each thread the experts it goes on with)
+    float sum = s_sum[e];
+#pragma unroll
+    for (int i = 1; i < kSlots; ++i) sum += s_sum[i * a.E + e];
+    s_sum[e] = sum;
   }
 
   if (gridDim.x > 1) {
@@ -224,7 +236,7 @@ __global__ __launch_bounds__(kBalanceWaves * 64, 2) void balance_stats_kernel(Ba
   if (lane == 0) s_dot[wave] = dot;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kBalanceWaves; ++w) dot += s_dot[w];
+    for (int w = 1; w < kWaves; ++w) dot += s_dot[w];
     const int n = s_tokens;
     a.tokens[0] = n;
     a.loss[0] = n > 0 && s_routed > 0
@@ -234,76 +246,89 @@ __global__ __launch_bounds__(kBalanceWaves * 64, 2) void balance_stats_kernel(Ba
   }
 }
 
-// The workgroups' sums and counts into the call's: 64 experts per workgroup, its sixteen
-// wavefronts over the G parts.  The workgroup that comes last adds up the loss.
-constexpr int kJoinWaves = 16;
-__global__ __launch_bounds__(kJoinWaves * 64) void balance_join_kernel(BalanceArgs a, int G) {
-  __shared__ double s_sum[kJoinWaves][64];
-  __shared__ int32_t s_count[kJoinWaves][64];
-  __shared__ int32_t s_tokens[kJoinWaves];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int e = static_cast<int>(blockIdx.x) * 64 + lane;
+// The workgroups' sums and counts into the call's: sixteen experts per workgroup, its 64 groups of
+// sixteen lanes over the G parts.  The workgroup that comes last adds up the loss.
+constexpr int kJoinGroups = 64, kJoinExperts = kBalanceJoinExperts;
+__global__ __launch_bounds__(kJoinGroups * kJoinExperts) void balance_join_kernel(BalanceArgs a, int G) {
+  __shared__ double s_sum[kJoinGroups][kJoinExperts];
+  __shared__ int32_t s_count[kJoinGroups][kJoinExperts];
+  __shared__ int32_t s_tokens[16];
+  const int tid = threadIdx.x, group = tid / kJoinExperts, col = tid % kJoinExperts;
+  const int e = static_cast<int>(blockIdx.x) * kJoinExperts + col;
   double sum = 0.0;
   int32_t count = 0;
   if (e < a.E) {
-#pragma unroll 8
-    for (int g = wave; g < G; g += kJoinWaves) {
+#pragma unroll 4
+    for (int g = group; g < G; g += kJoinGroups) {
       sum += a.part_sums[static_cast<int64_t>(g) * a.E + e];
       count += a.part_counts[static_cast<int64_t>(g) * a.E + e];
     }
   }
-  s_sum[wave][lane] = sum;
-  s_count[wave][lane] = count;
-  int32_t tokens = 0;
+  s_sum[group][col] = sum;
+  s_count[group][col] = count;
   if (blockIdx.x == 0) {
-    for (int g = threadIdx.x; g < G; g += kJoinWaves * 64) tokens += a.part_tokens[g];
+    int32_t tokens = 0;
+    for (int g = tid; g < G; g += kJoinGroups * kJoinExperts) tokens += a.part_tokens[g];
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) tokens += __shfl_xor(tokens, off);
-    if (lane == 0) s_tokens[wave] = tokens;
+    if ((tid & 63) == 0) s_tokens[tid >> 6] = tokens;
   }
   __syncthreads();
-  if (wave == 0) {
-    for (int w = 1; w < kJoinWaves; ++w) {
-      sum += s_sum[w][lane];
-      count += s_count[w][lane];
-    }
-    const float s = static_cast<float>(sum);
-    if (e < a.E) {
-      a.sums[e] = s;
-      a.counts[e] = count;
-    }
-    double dot = static_cast<double>(count) * s;
-    int64_t routed = count;
+  if (tid >= 64) return;
+  // four quarters of the groups, then those
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-      dot += __shfl_xor(dot, off);
-      routed += __shfl_xor(routed, off);
+  for (int i = 4; i < kJoinGroups; i += 4) {
+    sum += s_sum[group + i][col];
+    count += s_count[group + i][col];
+  }
+#pragma unroll
+  for (int off = kJoinExperts; off < 64; off <<= 1) {
+    sum += __shfl_xor(sum, off);
+    count += __shfl_xor(count, off);
+  }
+  const float s = static_cast<float>(sum);
+  if (group == 0 && e < a.E) {
+    a.sums[e] = s;
+    a.counts[e] = count;
+  }
+  double dot = static_cast<double>(count) * s;
+  int64_t routed = count;
+#pragma unroll
+  for (int off = kJoinExperts / 2; off > 0; off >>= 1) {
+    dot += __shfl_xor(dot, off);
+    routed += __shfl_xor(routed, off);
+  }
+  bool last = false;
+  if (tid == 0) {
+    a.part_dot[blockIdx.x] = dot;
+    a.part_routed[blockIdx.x] = routed;
+    if (blockIdx.x == 0) {
+      int32_t n = 0;
+      for (int w = 0; w < 16; ++w) n += s_tokens[w];
+      a.tokens[0] = n;
     }
-    if (lane == 0) {
-      a.part_dot[blockIdx.x] = dot;
-      a.part_routed[blockIdx.x] = routed;
-      if (blockIdx.x == 0) {
-        int32_t n = 0;
-        for (int w = 0; w < kJoinWaves; ++w) n += s_tokens[w];
-        a.tokens[0] = n;
-      }
-      __threadfence();
-      const bool last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
-      __threadfence();
-      if (last) {
-        dot = 0.0;
-        routed = 0;
-        for (unsigned b = 0; b < gridDim.x; ++b) {
-          dot += __hip_atomic_load(a.part_dot + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          routed += __hip_atomic_load(a.part_routed + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        const int32_t n = __hip_atomic_load(a.tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        a.loss[0] = n > 0 && routed > 0
-                        ? static_cast<float>(static_cast<double>(a.coef) * a.E * dot /
-                                             (static_cast<double>(n) * static_cast<double>(routed)))
-                        : 0.0f;
-      }
-    }
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    __threadfence();
+  }
+  if (!__shfl(static_cast<int>(last), 0)) return;
+  dot = 0.0;
+  routed = 0;
+  for (unsigned b = tid; b < gridDim.x; b += 64) {
+    dot += __hip_atomic_load(a.part_dot + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    routed += __hip_atomic_load(a.part_routed + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    dot += __shfl_xor(dot, off);
+    routed += __shfl_xor(routed, off);
+  }
+  if (tid == 0) {
+    const int32_t n = __hip_atomic_load(a.tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    a.loss[0] = n > 0 && routed > 0
+                    ? static_cast<float>(static_cast<double>(a.coef) * a.E * dot /
+                                         (static_cast<double>(n) * static_cast<double>(routed)))
+                    : 0.0f;
   }
 }
 
@@ -314,16 +339,17 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
   const int step = static_cast<int>(gridDim.x) * 4 * kRows;
   int t = (static_cast<int>(blockIdx.x) * 4 + wave) * kRows + lane / LPR;
   auto counted = [&](int row) { return row < a.T && (!a.mask || a.mask[row]); };
-  auto fetch = [&](int row, float (&to)[V]) {
-    if (counted(row)) {
-      load_row<BF16, LPR, V, VEC>(a.logits, row, a.E, sub, -__builtin_inff(), to);
+  auto fetch = [&](int row, bool live, float (&to)[V]) {
+    if (live) {
+      load_row<BF16, LPR, V, VEC, true>(a.logits, row, a.E, sub, -__builtin_inff(), to);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) to[v] = -__builtin_inff();
     }
   };
   float z[V], d[V];
-  fetch(t, z);
+  bool live = counted(t), live_next = counted(t + step);
+  fetch(t, live, z);
   // centred counts
   double all = 0.0;
 #pragma unroll
@@ -347,12 +373,13 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
   for (int base = t - lane / LPR; base < a.T; base += step, t += step) {   // whole wavefronts
     float next[V], more[V];
     if (a.add && t < a.T) {
-      load_row<BF16, LPR, V, VEC>(a.add, t, a.E, sub, 0.0f, more);
+      load_row<BF16, LPR, V, VEC, true>(a.add, t, a.E, sub, 0.0f, more);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) more[v] = 0.0f;
     }
-    fetch(t + step, next);
+    fetch(t + step, live_next, next);
+    const bool live_then = counted(t + 2 * step);
     const float inv = softmax_parts<LPR, V>(z);
     float dot = 0.0f;
 #pragma unroll
@@ -360,7 +387,6 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
     dot = row_sum<LPR>(dot) * inv;
     if (t < a.T) {
       const float f = scale * inv;
-      const bool live = counted(t);
       float o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -372,11 +398,12 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
           const int e = 4 * (sub + LPR * i);
           if (e >= a.E) continue;
           if constexpr (BF16)
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.grad) + at + e) =
-                u32x2{pack_bf16x2(o[4 * i], o[4 * i + 1]), pack_bf16x2(o[4 * i + 2], o[4 * i + 3])};
+            __builtin_nontemporal_store(
+                u32x2{pack_bf16x2(o[4 * i], o[4 * i + 1]), pack_bf16x2(o[4 * i + 2], o[4 * i + 3])},
+                reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.grad) + at + e));
           else
-            *reinterpret_cast<f32x4*>(static_cast<float*>(a.grad) + at + e) =
-                f32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+            __builtin_nontemporal_store(f32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]},
+                                        reinterpret_cast<f32x4*>(static_cast<float*>(a.grad) + at + e));
         }
       } else {
 #pragma unroll
@@ -390,6 +417,8 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) z[v] = next[v];
+    live = live_next;
+    live_next = live_then;
   }
 }
 
@@ -407,19 +436,24 @@ static void for_experts(int E, F f) {
   else f(RowC<64>{}, RowC<64>{});
 }
 
+// Workgroups of the first launch.  One that takes all rows, up to four a wavefront, is a call of
+// one launch: 64 tokens of 896 experts 11.1 us, 14.1 with eight workgroups and a second launch.
+// 16384 x 896 logits take 19 us, 13 the first launch (4.1 TB/s) and 5.6 the second; with two rows
+// ahead instead of one 21.
 int balance_parts(int T, int E) {
-  const int rows = kBalanceWaves * (E <= 16 ? 16 : E <= 64 ? 4 : 1);
-  const int G = (T + rows - 1) / rows;
-  return G < kBalanceMaxParts ? G : kBalanceMaxParts;
+  const int rows = balance_waves(E <= 1024 ? 16 : 64) * (E <= 16 ? 16 : E <= 64 ? 4 : 1);
+  if (T <= 4 * rows) return 1;
+  const int G = (T + rows - 1) / rows, most = E <= 1024 ? kBalanceMaxParts / 2 : kBalanceMaxParts;
+  return G < most ? G : most;
 }
 
 hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream) {
   const int G = balance_parts(a.T, a.E);
   const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (a.bf16 ? 8 : 16) == 0;
-  const size_t lds = static_cast<size_t>(a.E) * 8;
   for_experts(a.E, [&](auto lpr, auto v) {
     constexpr int L = decltype(lpr)::value, V = decltype(v)::value;
-    const dim3 grid(static_cast<unsigned>(G)), block(kBalanceWaves * 64);
+    const dim3 grid(static_cast<unsigned>(G)), block(balance_waves(V) * 64);
+    const size_t lds = static_cast<size_t>(a.E) * 4 * (balance_slots(V) + 1);
     if (a.bf16) {
       if (vec) balance_stats_kernel<true, L, V, true><<<grid, block, lds, stream>>>(a);
       else balance_stats_kernel<true, L, V, false><<<grid, block, lds, stream>>>(a);
@@ -430,19 +464,23 @@ hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream) {
   });
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess || G == 1) return err;
-  balance_join_kernel<<<dim3(static_cast<unsigned>((a.E + 63) / 64)), dim3(kJoinWaves * 64), 0,
-                        stream>>>(a, G);
+  const unsigned joins = static_cast<unsigned>((a.E + kJoinExperts - 1) / kJoinExperts);
+  balance_join_kernel<<<dim3(joins), dim3(kJoinGroups * kJoinExperts), 0, stream>>>(a, G);
   return hipGetLastError();
 }
 
+// Bound by the bytes: 16384 x 896 logits and as many values added (170 MB) 37 us, 4.6 TB/s (a large
+// copy on the same card 5.1).  As many workgroups as the CUs hold at once (each goes on to further
+// rows), and the rows go past the caches both ways: with eight workgroups per CU whatever the
+// registers 42 us, through the caches 46; 8192 x 2048 logits 32 us and 58.
 hipError_t launch_balance_loss_grad(const BalanceGradArgs& a, hipStream_t stream) {
-  const int rows = 4 * (a.E <= 16 ? 16 : a.E <= 64 ? 4 : 1);
-  const int blocks = (a.T + rows - 1) / rows, most = 8 * a.cus;
+  const int rows = 4 * (a.E <= 16 ? 16 : a.E <= 64 ? 4 : 1), blocks = (a.T + rows - 1) / rows;
   const uintptr_t all = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.add) |
                         reinterpret_cast<uintptr_t>(a.grad);
   const bool vec = a.E % 4 == 0 && all % (a.bf16 ? 8 : 16) == 0;
   for_experts(a.E, [&](auto lpr, auto v) {
     constexpr int L = decltype(lpr)::value, V = decltype(v)::value;
+    const int most = a.cus * (V <= 8 ? 8 : V <= 16 ? 5 : V <= 32 ? 3 : 1);
     const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most)), block(256);
     if (a.bf16) {
       if (vec) balance_grad_kernel<true, L, V, true><<<grid, block, 0, stream>>>(a);

@@ -243,7 +243,7 @@ hipError_t launch_quantize_mxfp4(const MxRowsArgs& a, hipStream_t stream);
 hipError_t launch_dequantize_mxfp4(const MxRowsArgs& a, hipStream_t stream);
 
 // The router's balance loss and its gradient (balance.hip).
-constexpr int kBalanceMaxParts = 512;
+constexpr int kBalanceMaxParts = 512, kBalanceJoinExperts = 16;
 struct BalanceArgs {
   int T, E, k;
   const void* logits;          // [T, E] fp32 or BF16
