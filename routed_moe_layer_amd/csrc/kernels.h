@@ -228,6 +228,8 @@ struct MxGroupedArgs : GroupedArgs {
   int SB;                      // a multiple of 4, at least K/32
 };
 hipError_t launch_grouped_mxfp4(const MxGroupedArgs& a, hipStream_t stream);
+// The largest tiles (grouped_mxfp4_big.hip): at most 1024 experts, operands within 32-bit offsets.
+hipError_t launch_grouped_mxfp4_big(const MxGroupedArgs& a, hipStream_t stream);
 
 // Microscaled FP4 rows and back (mxfp4.hip).
 struct MxRowsArgs {
