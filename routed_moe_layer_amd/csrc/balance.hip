@@ -366,7 +366,8 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
     d[v] = e < a.E ? static_cast<float>(a.counts[e] - mean) : 0.0f;
   }
   const double n = a.tokens[0];
-  const float scale = n > 0.0 && all > 0.0
+  const bool some = n > 0.0 && all > 0.0;              // without, NaN rows have no gradient either
+  const float scale = some
                           ? static_cast<float>(static_cast<double>(a.coef) * a.E / (n * all)) *
                                 (a.grad_loss ? a.grad_loss[0] : 1.0f)
                           : 0.0f;
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
       float o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        o[v] = live ? __builtin_fmaf(f * z[v], d[v] - dot, more[v]) : more[v];
+        o[v] = live && some ? __builtin_fmaf(f * z[v], d[v] - dot, more[v]) : more[v];
       const int64_t at = static_cast<int64_t>(t) * a.E;
       if constexpr (VEC) {
 #pragma unroll

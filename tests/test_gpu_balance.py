@@ -161,6 +161,22 @@ def test_nothing_counted(T, E):
     assert torch.equal(_grad(z, None, counts, tokens, add=add), add)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,E", [(6, 10), (40, 896), (300, 130)])
+def test_nothing_counted_in_rows_of_nan(T, E, bf16):
+    """The loss is 0 and its gradient what is added, whatever the probabilities are."""
+    _say(f"balance nothing of NaN T={T} E={E} bf16={bf16}")
+    g = _gen(9)
+    z = _logits(g, T, E, bf16)
+    z[::2, 1], z[1, 2] = NAN, INF
+    add = _normal(g, T, E, dtype=z.dtype)
+    ids = torch.full((T, 3), -1, dtype=I32, device="cuda")
+    counts, sums, tokens, loss = _loss(z, ids, None)
+    assert float(loss) == 0 and int(tokens) == T and not bool(counts.any())
+    assert not bool(_grad(z, None, counts, tokens).any())
+    assert torch.equal(_grad(z, None, counts, tokens, add=add), add)
+
+
 @pytest.mark.parametrize("T,E", [(20, 12), (20, 50), (100, 896), (9, 4096)])
 def test_experts_that_a_token_cannot_take(T, E):
     """Logits of -inf and of the type's lowest value; a row of nothing else; a NaN and a +inf."""
