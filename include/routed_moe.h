@@ -448,7 +448,9 @@ moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, i
 /* moe_grouped_gemm with both operands in MXFP4: rows, experts, prefix sums, source rows and the
  * epilogue as there, with
  *   h[i, n] = sum_b 2^(sx[b] - 127) 2^(sw[n, b] - 127) sum_{j < 32} X[i, 32b + j] W_e[n, 32b + j]
- * over blocks b of K; the products of one block are added exactly, the blocks in fp32.
+ * over blocks b of K; the products of one block are added exactly, the blocks in fp32, in
+ * an order that goes with the sizes: sums whose parts leave fp32's range are infinite or NaN, as is every product
+ * with a block of scale byte 255 (NaN), with zeros and rows without a source too.
  * Buffers (device): x_codes u8 [x_rows, K/2] and x_scales u8 [x_rows, MOE_MXFP4_SCALE_STRIDE(K)];
  * w_codes u8 [E, Nw, K/2] and w_scales u8 [E, Nw, MOE_MXFP4_SCALE_STRIDE(K)]; row_idx,
  * expert_cumsum, situ_beta, situ_linear_beta and out as at moe_grouped_gemm.
