@@ -26,8 +26,9 @@ __device__ __forceinline__ void mx_mma_in_place(u32x4 a, u32x4 b, f32x4& acc, ui
 // (Inside a batch only LDS reads write operands, which are waited for.  An s_nop in front of each
 // instruction took 4% of 8192^3.)
 __device__ __forceinline__ void ready() { asm volatile("s_nop 1" ::: "memory"); }
-// Behind the last of them in a loop, before its branch: a 4-pass instruction's result is there
-// after 7 wait states, and code behind the loop may read it at once.
+// Behind the last of them in a loop, before its branch: on gfx950 a 4-pass instruction's result is
+// there after eight wait states, and code behind the loop may read it at once.  s_nop 7 is exactly
+// those eight, as the compiler puts behind the builtin; there is none to spare.
 __device__ __forceinline__ void settle() { asm volatile("s_nop 7" ::: "memory"); }
 
 // ---------------------------------------------------------------------------------------
