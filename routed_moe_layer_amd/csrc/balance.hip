@@ -384,17 +384,22 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
 #pragma unroll
   for (int off = 1; off < LPR; off <<= 1) all += __shfl_xor(all, off);
   const double mean = all / a.E;
+  const double n = a.tokens[0];
+  const bool some = n > 0.0 && all > 0.0;              // without, NaN rows have no gradient either
+  // The scale may lie far outside fp32's range where the gradient does not: half of its power of two
+  // goes to the counts (at most 2^95, so that 31 bits of counts stay below 2^127), and what then is
+  // still above 2^95 to the result.  (Far below, nothing is left of any gradient.)
+  const double whole = some ? static_cast<double>(a.coef) * a.E / (n * all) *
+                                  (a.grad_loss ? a.grad_loss[0] : 1.0f)
+                            : 0.0;
+  const int power = __builtin_amdgcn_frexp_exp(whole), half = min(max(power / 2, -95), 95);
+  const int above = __builtin_amdgcn_readfirstlane(max(power - 190, 0));
+  const float scale = static_cast<float>(ldexp(whole, -half - above));
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = expert_of<LPR, VEC>(sub, v);
-    d[v] = e < a.E ? static_cast<float>(a.counts[e] - mean) : 0.0f;
+    d[v] = e < a.E ? ldexpf(static_cast<float>(a.counts[e] - mean), half) : 0.0f;
   }
-  const double n = a.tokens[0];
-  const bool some = n > 0.0 && all > 0.0;              // without, NaN rows have no gradient either
-  const float scale = some
-                          ? static_cast<float>(static_cast<double>(a.coef) * a.E / (n * all)) *
-                                (a.grad_loss ? a.grad_loss[0] : 1.0f)
-                          : 0.0f;
   for (int base = t - lane / LPR; base < a.T; base += step, t += step) {   // whole wavefronts
     float next[V], more[V];
     if (a.add && t < a.T) {
@@ -414,8 +419,11 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
       const float f = scale * inv;
       float o[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        o[v] = live && some ? __builtin_fmaf(f * z[v], d[v] - dot, more[v]) : more[v];
+      for (int v = 0; v < V; ++v) {
+        const float p = f * z[v], c = d[v] - dot;
+        const float sum = above == 0 ? __builtin_fmaf(p, c, more[v]) : ldexpf(p * c, above) + more[v];
+        o[v] = live && some ? sum : more[v];
+      }
       const int64_t at = static_cast<int64_t>(t) * a.E;
       if constexpr (VEC) {
 #pragma unroll
