@@ -3,6 +3,7 @@
 #include "routed_moe.h"
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "common.h"
@@ -1030,7 +1031,7 @@ moe_status_t moe_balance_loss(int32_t T, int32_t num_experts, int32_t top_k, con
   if (st != MOE_OK) return st;
   if (top_k < 1) return MOE_ERR_INVALID_ARG;
   if (top_k > 64) return MOE_ERR_UNSUPPORTED;
-  if (!(coef >= -3.4e38f && coef <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(coef)) return MOE_ERR_INVALID_ARG;
   if (!logits || !expert_ids || !counts || !prob_sums || !tokens || !loss || !workspace)
     return MOE_ERR_INVALID_ARG;
   if (!aligned(logits, logits_are_bf16 ? 2 : 4) || !aligned(expert_ids, 4) ||
@@ -1053,7 +1054,7 @@ moe_status_t moe_balance_loss_grad(int32_t T, int32_t num_experts, const void* l
                                    moe_stream_t stream) {
   moe_status_t st = balance_dims(T, num_experts);
   if (st != MOE_OK) return st;
-  if (!(coef >= -3.4e38f && coef <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(coef)) return MOE_ERR_INVALID_ARG;
   if (!logits || !counts || !tokens || !grad_logits) return MOE_ERR_INVALID_ARG;
   const size_t value = logits_are_bf16 ? 2 : 4;
   if (!aligned(logits, value) || !aligned(counts, 4) || !aligned(tokens, 4) ||
