@@ -72,8 +72,8 @@ struct MxItemWalk {
 // ---------------------------------------------------------------------------------------
 // Tiles of up to BM rows (16, 32, 64 or 128).  A workgroup of NW wavefronts multiplies one tile of
 // an expert's rows with 32 NW weight rows, 32 per wavefront.  Codes and scales of both operands
-// go from memory straight into LDS in chunks of 128 bytes of K, in a ring of S chunks that runs on
-// over the borders between items: the load side is S - 1 chunks ahead of the products, with items
+// go from memory straight into LDS in chunks of 128 bytes of K, in a ring of three that runs on
+// over the borders between items: the load side is two chunks ahead of the products, with items
 // of its own.  Every wavefront issues the same number of loads per chunk (the token rows' scales
 // are loaded by several wavefronts alike), so one counted wait per chunk is enough: a chunk is
 // there when no more loads are under way than were issued after it (stores behind them only make
@@ -91,8 +91,9 @@ struct MxItemWalk {
 // with the loads around them.  Otherwise they are the sorted rows themselves or, of at most
 // kMxListRows, in a list in LDS.
 constexpr int kMxListRows = 2048;
+constexpr int kMxRing = 3;                             // chunks in LDS
 
-template <bool SITU, bool DIRECT, bool WIDE, int BM, int NW, int PER_CU, int S>
+template <bool SITU, bool DIRECT, bool WIDE, int BM, int NW, int PER_CU>
 __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid_kernel(MxGroupedArgs a) {
   constexpr int kRows = 32 * NW, kCols = kRows / (SITU ? 2 : 1), MT = BM / 16;
   constexpr int kXLoads = BM / (8 * NW), kLoads = 6 + kXLoads;       // per wavefront and chunk
@@ -103,11 +104,8 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
   extern __shared__ int32_t s_tile[];
   __shared__ alignas(16) uint8_t s_0[kBytes], s_1[kBytes], s_2[kBytes];
   auto ring = [&](auto u) {
-    constexpr int U = decltype(u)::value % S;
-    if constexpr (U == 0) return &s_0[0];
-    else if constexpr (U == 1) return &s_1[0];
-    else if constexpr (U == 2) return &s_2[0];
-    else return more_ring<U, kBytes>();
+    constexpr int U = decltype(u)::value % kMxRing;
+    return U == 0 ? &s_0[0] : U == 1 ? &s_1[0] : &s_2[0];
   };
   mx_scan<NW>(a, s_tile, a.R / BM + min(a.R, a.E), [](int n) { return (n + BM - 1) / BM; });
   const int nblk = (a.N + kCols - 1) / kCols;
@@ -252,7 +250,7 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
   // next loads write; after the barrier that holds for the workgroup
   auto arrive = [&]() {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm_lds((S - 2) * kLoads));
+    __builtin_amdgcn_s_waitcnt(wait_vm_lds((kMxRing - 2) * kLoads));
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -327,7 +325,7 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
 
   prepare();
   begin_item();
-  for_ring<S - 1>([&](auto u) { load(ring(u)); });
+  for_ring<kMxRing - 1>([&](auto u) { load(ring(u)); });
   clear();
   // An item may end at any buffer of the ring.  The steps of a round are taken whatever happens in
   // it, behind the last item on chunks that nobody stores: with a step left out on some path the
@@ -335,9 +333,9 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
   int c = 0;
   bool alive = true;
   while (alive) {
-    for_ring<S>([&](auto u) __attribute__((always_inline)) {
+    for_ring<kMxRing>([&](auto u) __attribute__((always_inline)) {
       arrive();
-      load(ring(IntC<decltype(u)::value + S - 1>{}));
+      load(ring(IntC<decltype(u)::value + kMxRing - 1>{}));
       compute(ring(u));
       if (++c == nc) {
         c = 0;
@@ -358,16 +356,16 @@ static bool mx_wide(const MxGroupedArgs& a) {
          (a.row_idx && static_cast<uint64_t>(a.x_rows) * a.KB > kBufferMost);
 }
 
-template <bool SITU, bool WIDE, int BM, int NW, int PER_CU, int S>
+template <bool SITU, bool WIDE, int BM, int NW, int PER_CU>
 static hipError_t launch_mx_mid(const MxGroupedArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.cus / a.xcds * a.xcds * PER_CU)), block(NW * 64);
   // the list has to fit behind the ring too (160 KB, less what the scan takes)
-  constexpr size_t kRing = S * ((32 * NW + BM) * 128 + (32 * NW + (BM < 32 ? 32 : BM)) * 8);
+  constexpr size_t kRing = kMxRing * ((32 * NW + BM) * 128 + (32 * NW + (BM < 32 ? 32 : BM)) * 8);
   const size_t starts = (static_cast<size_t>(a.E) + 1) * 4, list = a.row_idx ? size_t(a.R) * 4 : 0;
   const bool direct = a.row_idx && (a.R > kMxListRows || kRing + starts + list > 163840 - 128);
   const size_t lds = starts + (direct ? 0 : list);
-  if (direct) grouped_mx_mid_kernel<SITU, true, WIDE, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
-  else grouped_mx_mid_kernel<SITU, false, WIDE, BM, NW, PER_CU, S><<<grid, block, lds, stream>>>(a);
+  if (direct) grouped_mx_mid_kernel<SITU, true, WIDE, BM, NW, PER_CU><<<grid, block, lds, stream>>>(a);
+  else grouped_mx_mid_kernel<SITU, false, WIDE, BM, NW, PER_CU><<<grid, block, lds, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -392,22 +390,22 @@ static hipError_t launch_mx_one(const MxGroupedArgs& a, hipStream_t stream) {
   auto items = [&](int tile, int block) { return (some + R / tile) * ((a.Nw + block - 1) / block); };
   // (operands past the descriptors' reach, whose loads cost more, are not worth more kernels than two)
   if (mx_wide(a)) {
-    if (R > 8 * some) return launch_mx_mid<SITU, true, 64, 4, 2, 3>(a, stream);
-    return launch_mx_mid<SITU, true, 16, 2, 4, 3>(a, stream);
+    if (R > 8 * some) return launch_mx_mid<SITU, true, 64, 4, 2>(a, stream);
+    return launch_mx_mid<SITU, true, 16, 2, 4>(a, stream);
   }
   // (the LDS of the larger tiles leaves room for so many experts' prefix sums)
   const int64_t items256 = items(256, 256);
   if (E <= 1024 && items256 >= few && (R >= 448 * E || (R >= 224 * E && items256 <= a.cus)))
     return launch_grouped_mxfp4_big(a, stream);
   if (items(128, 256) >= few) {
-    if (E <= 1536 && R > 32 * E) return launch_mx_mid<SITU, false, 128, 8, 1, 3>(a, stream);
-    if (E <= 8192 && R > 8 * E) return launch_mx_mid<SITU, false, 64, 8, 1, 3>(a, stream);
-    if (R > 8 * E) return launch_mx_mid<SITU, false, 64, 4, 2, 3>(a, stream);
+    if (E <= 1536 && R > 32 * E) return launch_mx_mid<SITU, false, 128, 8, 1>(a, stream);
+    if (E <= 8192 && R > 8 * E) return launch_mx_mid<SITU, false, 64, 8, 1>(a, stream);
+    if (R > 8 * E) return launch_mx_mid<SITU, false, 64, 4, 2>(a, stream);
   } else if (R > 16 * some) {
-    if (items(64, 128) >= few) return launch_mx_mid<SITU, false, 64, 4, 2, 3>(a, stream);
-    return launch_mx_mid<SITU, false, 32, 2, 4, 3>(a, stream);
+    if (items(64, 128) >= few) return launch_mx_mid<SITU, false, 64, 4, 2>(a, stream);
+    return launch_mx_mid<SITU, false, 32, 2, 4>(a, stream);
   }
-  return launch_mx_mid<SITU, false, 16, 2, 4, 3>(a, stream);
+  return launch_mx_mid<SITU, false, 16, 2, 4>(a, stream);
 }
 
 hipError_t launch_grouped_mxfp4(const MxGroupedArgs& a, hipStream_t stream) {
