@@ -4,10 +4,10 @@
 
 #include "common.h"
 #include "grouped.h"
+#include "grouped_mxfp4_rule.h"
 #include "kernels.h"
 
 namespace rmoe {
-
 
 // A row's 16-byte pieces lie in the eight slots of its 128 bytes of LDS, piece p in slot
 // p ^ mx_swizzle(row).  A fragment read takes pieces 2 g + f of sixteen rows; the LDS serves it in
@@ -67,7 +67,7 @@ __device__ __forceinline__ void store_columns(uint16_t* o, uint2 v, int N, int n
 // expert's, and its token rows those of a tile where nothing gathers them) it is three or four more,
 // and a chunk's loads were most of what a wavefront did.
 typedef __amdgpu_buffer_rsrc_t buffer_t;
-constexpr uint32_t kNowhere = 0xFFFF0000u, kBufferMost = kNowhere;
+constexpr uint32_t kNowhere = kMxBufferMost;
 __device__ __forceinline__ buffer_t mx_buffer(const uint8_t* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(bytes),
                                            0x00020000);

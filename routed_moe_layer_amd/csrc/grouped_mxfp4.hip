@@ -13,10 +13,9 @@
 // A K chunk is 128 bytes of codes per row, eight blocks and two dwords of scales.  Its order in K
 // is free as long as both operands agree: fragment f of lane group g takes block 2 g + f, so that
 // a lane's two scale bytes lie next to each other and the instruction's byte selector is f.
-#include <algorithm>
-
 #include "common.h"
 #include "grouped_mxfp4.h"
+#include "grouped_mxfp4_rule.h"
 #include "kernels.h"
 
 namespace rmoe {
@@ -90,8 +89,6 @@ struct MxItemWalk {
 // DIRECT: the source rows of a tile are read from row_idx, which the wavefront has to wait for
 // with the loads around them.  Otherwise they are the sorted rows themselves or, of at most
 // kMxListRows, in a list in LDS.
-constexpr int kMxListRows = 2048;
-constexpr int kMxRing = 3;                             // chunks in LDS
 
 template <bool SITU, bool DIRECT, bool WIDE, int BM, int NW, int PER_CU>
 __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid_kernel(MxGroupedArgs a) {
@@ -101,6 +98,7 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
   static_assert(kXLoads * 8 * NW == BM && kXScaleLoads <= NW, "");
   // a buffer: weights, token rows, the weights' scales, the token rows' scales
   constexpr int kScales = (kRows + BM) * 128, kBytes = kScales + (kRows + 32 * kXScaleLoads) * 8;
+  static_assert(kMxRing * kBytes == mx_ring_bytes(MxTiles{BM, NW, PER_CU, WIDE}), "");
   extern __shared__ int32_t s_tile[];
   __shared__ alignas(16) uint8_t s_0[kBytes], s_1[kBytes], s_2[kBytes];
   auto ring = [&](auto u) {
@@ -350,62 +348,29 @@ __global__ __launch_bounds__(NW * 64, (NW * PER_CU + 3) / 4) void grouped_mx_mid
   __builtin_amdgcn_s_waitcnt(0);                       // no load into LDS outlives the workgroup
 }
 
-// Operands past what a buffer descriptor reaches.
-static bool mx_wide(const MxGroupedArgs& a) {
-  return static_cast<uint64_t>(a.Nw) * a.KB > kBufferMost ||
-         (a.row_idx && static_cast<uint64_t>(a.x_rows) * a.KB > kBufferMost);
-}
-
 template <bool SITU, bool WIDE, int BM, int NW, int PER_CU>
-static hipError_t launch_mx_mid(const MxGroupedArgs& a, hipStream_t stream) {
+static hipError_t launch_mx_mid(const MxGroupedArgs& a, const MxSizes& s, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.cus / a.xcds * a.xcds * PER_CU)), block(NW * 64);
-  // the list has to fit behind the ring too (160 KB, less what the scan takes)
-  constexpr size_t kRing = kMxRing * ((32 * NW + BM) * 128 + (32 * NW + (BM < 32 ? 32 : BM)) * 8);
-  const size_t starts = (static_cast<size_t>(a.E) + 1) * 4, list = a.row_idx ? size_t(a.R) * 4 : 0;
-  const bool direct = a.row_idx && (a.R > kMxListRows || kRing + starts + list > 163840 - 128);
-  const size_t lds = starts + (direct ? 0 : list);
+  const bool direct = mx_direct(s, MxTiles{BM, NW, PER_CU, WIDE});
+  const size_t list = a.row_idx && !direct ? size_t(a.R) * 4 : 0;
+  const size_t lds = (static_cast<size_t>(a.E) + 1) * 4 + list;
   if (direct) grouped_mx_mid_kernel<SITU, true, WIDE, BM, NW, PER_CU><<<grid, block, lds, stream>>>(a);
   else grouped_mx_mid_kernel<SITU, false, WIDE, BM, NW, PER_CU><<<grid, block, lds, stream>>>(a);
   return hipGetLastError();
 }
 
-// Which kernel.  Larger tiles read the weights for more rows at once; smaller ones and smaller
-// blocks of weight rows make more work items.  items() is an upper bound of the items of a kernel
-// (the host does not know the rows of each expert), `few` three quarters of the CUs.  Measured on
-// one MI355X, us with tiles of 256 / 128 / 64 rows by 256 weight rows, 64 by 128, 32 by 64 and 16
-// by 64:
-//   many rows per expert: 64 experts x 512 rows, N = K = 2048  130 / 146 / 190 / 183 / 287 / 438;
-//     x 256 rows (half of the experts above one tile)  80 / 84 / 103 / 100 / 157 / 230, but 896 x
-//     292 rows, N = 384 with SiTU, K = 3584  986 / 872 / 1138 / 1373 / 2282 / 2614; 8 x 256 rows,
-//     N = K = 4096, whose tiles of 256 are one round of the chip  43 / 55 / 58 / 52 / 76 / 109;
-//   fewer: 896 x 73 rows, the same N and K  440 / 347 / 458 / 522 / 707 / 798; 18 rows, N = 3584,
-//     K = 384, Zipf  345 / 216 / 210 / 284 / 321 / 251; 4.6 rows  288 / 202 / 186 / 240 / 237 / 158;
-//     1.1 rows, N = 384 with SiTU, K = 3584  112 / 77 / 76 / 85 / 83 / 72;
-//   few items: 8 experts x 32 rows, N = K = 4096  26 / 24 / 24 / 18 / 24 / 28; one expert, N = K =
-//     7168, 512 rows  52 / 46 / 36 / 36 / 52 / 81, 64 rows  34 / 34 / 33 / 21 / 15 / 17, 16 rows
-//     33 / 29 / 28 / 18 / 13 / 13.
 template <bool SITU>
 static hipError_t launch_mx_one(const MxGroupedArgs& a, hipStream_t stream) {
-  const int64_t R = a.R, E = a.E, some = std::min(R, E), few = a.cus * 3 / 4;
-  auto items = [&](int tile, int block) { return (some + R / tile) * ((a.Nw + block - 1) / block); };
-  // (operands past the descriptors' reach, whose loads cost more, are not worth more kernels than two)
-  if (mx_wide(a)) {
-    if (R > 8 * some) return launch_mx_mid<SITU, true, 64, 4, 2>(a, stream);
-    return launch_mx_mid<SITU, true, 16, 2, 4>(a, stream);
-  }
-  // (the LDS of the larger tiles leaves room for so many experts' prefix sums)
-  const int64_t items256 = items(256, 256);
-  if (E <= 1024 && items256 >= few && (R >= 448 * E || (R >= 224 * E && items256 <= a.cus)))
-    return launch_grouped_mxfp4_big(a, stream);
-  if (items(128, 256) >= few) {
-    if (E <= 1536 && R > 32 * E) return launch_mx_mid<SITU, false, 128, 8, 1>(a, stream);
-    if (E <= 8192 && R > 8 * E) return launch_mx_mid<SITU, false, 64, 8, 1>(a, stream);
-    if (R > 8 * E) return launch_mx_mid<SITU, false, 64, 4, 2>(a, stream);
-  } else if (R > 16 * some) {
-    if (items(64, 128) >= few) return launch_mx_mid<SITU, false, 64, 4, 2>(a, stream);
-    return launch_mx_mid<SITU, false, 32, 2, 4>(a, stream);
-  }
-  return launch_mx_mid<SITU, false, 16, 2, 4>(a, stream);
+  const MxSizes s{a.R, a.E, a.Nw, a.KB, a.x_rows, a.row_idx != nullptr, a.cus};
+  const MxTiles t = mx_tiles(s);
+  if (t.rows == 256) return launch_grouped_mxfp4_big(a, stream);
+  if (t.rows == 128) return launch_mx_mid<SITU, false, 128, 8, 1>(a, s, stream);
+  if (t.rows == 64 && t.waves == 8) return launch_mx_mid<SITU, false, 64, 8, 1>(a, s, stream);
+  if (t.rows == 64 && t.wide) return launch_mx_mid<SITU, true, 64, 4, 2>(a, s, stream);
+  if (t.rows == 64) return launch_mx_mid<SITU, false, 64, 4, 2>(a, s, stream);
+  if (t.rows == 32) return launch_mx_mid<SITU, false, 32, 2, 4>(a, s, stream);
+  if (t.wide) return launch_mx_mid<SITU, true, 16, 2, 4>(a, s, stream);
+  return launch_mx_mid<SITU, false, 16, 2, 4>(a, s, stream);
 }
 
 hipError_t launch_grouped_mxfp4(const MxGroupedArgs& a, hipStream_t stream) {
