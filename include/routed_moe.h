@@ -426,7 +426,7 @@ moe_status_t moe_combine(int32_t T, int32_t H, int32_t k, int32_t R, const uint1
  *   moe_quantize_mxfp4 -> moe_grouped_gemm_mxfp4 (FC1, SiTU) -> moe_quantize_mxfp4 ->
  *   moe_grouped_gemm_mxfp4 (FC2) -> moe_combine
  * is an expert layer in 4 bits behind moe_route, with weights quantized once.  None of the three
- * needs a workspace.
+ * needs a workspace.  BF16 rows and codes are 16-byte aligned, scales 4-byte.
  * ------------------------------------------------------------------------------------ */
 #define MOE_MXFP4_SCALE_STRIDE(K) (((K) + 127) / 128 * 4)
 
@@ -448,9 +448,9 @@ moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, i
 /* moe_grouped_gemm with both operands in MXFP4: rows, experts, prefix sums, source rows and the
  * epilogue as there, with
  *   h[i, n] = sum_b 2^(sx[b] - 127) 2^(sw[n, b] - 127) sum_{j < 32} X[i, 32b + j] W_e[n, 32b + j]
- * over blocks b of K; the products of one block are added exactly, the blocks in fp32, in
- * an order that goes with the sizes: sums whose parts leave fp32's range are infinite or NaN, as is every product
- * with a block of scale byte 255 (NaN), with zeros and rows without a source too.
+ * over blocks b of K; the products of one block are added exactly, the blocks in fp32, in an
+ * order that goes with the sizes.  Sums whose parts leave fp32's range are infinite or NaN, and
+ * every product with a block of scale byte 255 is NaN, with zeros and rows without a source too.
  * Buffers (device): x_codes u8 [x_rows, K/2] and x_scales u8 [x_rows, MOE_MXFP4_SCALE_STRIDE(K)];
  * w_codes u8 [E, Nw, K/2] and w_scales u8 [E, Nw, MOE_MXFP4_SCALE_STRIDE(K)]; row_idx,
  * expert_cumsum, situ_beta, situ_linear_beta and out as at moe_grouped_gemm.
@@ -481,7 +481,8 @@ moe_status_t moe_grouped_gemm_mxfp4(int32_t R, int32_t N, int32_t K, int32_t E,
  * with g = *grad_loss (1 without), 0 + add for a masked token.  counts and tokens are
  * moe_balance_loss's, or their sums over the ranks of a data-parallel batch; where they say that
  * nothing was counted the gradient is add (0 without).
- * Sums are fp32 or wider and in a fixed order: a call's result is the same every time.
+ * Sums are fp32 or wider and in a fixed order: a call's result is the same every time.  The factor
+ * in front of p may leave fp32's range where the gradient does not.
  * Buffers (device): logits f32 [T, num_experts], or BF16 with logits_are_bf16 != 0, and add (or
  * NULL) and grad_logits of the same type; expert_ids i32 [T, top_k]; token_mask u8 [T] or NULL;
  * counts i32 [num_experts]; prob_sums f32 [num_experts]; tokens i32 [1]; loss f32 [1]; grad_loss

@@ -470,9 +470,11 @@ static void for_experts(int E, F f) {
 }
 
 // Workgroups of the first launch.  One that takes all rows, up to four a wavefront, is a call of
-// one launch: 64 tokens of 896 experts 11.1 us, 14.1 with eight workgroups and a second launch.
-// 16384 x 896 logits take 19 us, 13 the first launch (4.1 TB/s) and 5.6 the second; with two rows
-// ahead instead of one 21.
+// one launch.  us with one and with two launches: 48 x 896 10.1 / 11.5, 64 x 896 11.8 / 11.4 (BF16
+// 12.6 / 11.6), 64 x 512 8.9 / 11.4, 256 x 64 8.3 / 11.3, 32 x 2048 15.4 / 17.7, 32 x 4096 26.9 / 30.0
+// (BF16 31.2 / 31.4).  One workgroup is bound by what its CU issues: 64 x 896 are 16 rows a SIMD, about
+// 240 instructions each.  16384 x 896 logits take 20 us, 15.5 the first launch (3.8 TB/s) and 5.3 the
+// second; in BF16 21, which the same instructions bound and not the half as many bytes.
 int balance_parts(int T, int E) {
   const int rows = balance_waves(E <= 1024 ? 16 : 64) * (E <= 16 ? 16 : E <= 64 ? 4 : 1);
   if (T <= 4 * rows) return 1;
@@ -505,7 +507,9 @@ hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream) {
 // Bound by the bytes: 16384 x 896 logits and as many values added (170 MB) 37 us, 4.6 TB/s (a large
 // copy on the same card 5.1).  As many workgroups as the CUs hold at once (each goes on to further
 // rows), and the rows go past the caches both ways: with eight workgroups per CU whatever the
-// registers 42 us, through the caches 46; 8192 x 2048 logits 32 us and 58.
+// registers 42 us, through the caches 46; 8192 x 2048 logits 34 us and 58.  More than 2048 experts are
+// 64 values a lane in four arrays, one wavefront a SIMD, and where E is no multiple of four they come
+// one by one: 4096 x 4096 logits 41 us (BF16 58), 4096 x 4095 55 (BF16 115); the loss 59 and 62.
 hipError_t launch_balance_loss_grad(const BalanceGradArgs& a, hipStream_t stream) {
   const int rows = 4 * (a.E <= 16 ? 16 : a.E <= 64 ? 4 : 1), blocks = (a.T + rows - 1) / rows;
   const uintptr_t all = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.add) |

@@ -80,9 +80,10 @@ struct MxItemWalk {
 //
 // Bound by the bytes: FC1 of 16 tokens over 896 experts (N = 384 with SiTU, K = 3584, 328 MB) 71
 // us, 4.6 TB/s; FC1 of 4096 tokens (1.37 GB) 331 us, 4.1 TB/s; FC2 of 1024 Zipf tokens (N = 3584,
-// K = 384, 763 MB) 207 us, 3.7 TB/s, two chunks an item, half of the second of them zeros; a large
-// read on the same card 5.99 TB/s.  A CU takes in about 20 bytes a ns this way, whether they come
-// from memory or from a cache, and the token rows' count with the weights'.  Eight wavefronts per
+// K = 384, 763 MB) 209 us, 3.6 TB/s, two chunks an item, half of the second of them zeros; a large
+// read on the same card 5.99 TB/s.  A CU takes in 17 to 24 bytes a ns this way, however many of
+// them the L2 holds (of the three's requests 63, 44 and 53% miss it), and the token rows' count with the
+// weights'.  Eight wavefronts per
 // CU are needed for that: longer rings with four took 76 to 101 us for the 71.
 // ---------------------------------------------------------------------------------------
 //

@@ -46,10 +46,17 @@ __device__ __forceinline__ void settle() { asm volatile("s_nop 7" ::: "memory");
 // selector of the instruction.
 //
 // Bound by the matrix units, the LDS and the caches together and by the power they draw: 8192^3
-// takes 241 us, 4.6 PFLOP/s (the instruction alone on random codes 6.7, with the clock down to
-// 1.6 GHz; an earlier state at 4.0 made 4.6 without its loads and 4.7 without its LDS reads; the
-// library's product 2.9).  8 experts x 4096 rows (N = 3584, K = 4096) take 267 us, 3.6 PFLOP/s, in
-// seven to eight rounds of items.  Eight wavefronts of 128 x 64 products read 1.5 times as much from LDS.
+// takes 251 to 256 us, 4.3 to 4.4 PFLOP/s (the instruction alone on random codes 6.7, with the clock
+// down to 1.6 GHz; an earlier state at 4.0 made 4.6 without its loads and 4.7 without its LDS reads; the
+// library's product 2.9), the matrix units busy 53% of the cycles at 1.9 GHz.  8 experts x 4096 rows
+// (N = 3584, K = 4096) take 265 us, 3.6 PFLOP/s, in seven to eight rounds of items, 270 gathered: at a
+// change of item nine entries of row_idx are waited for one by one.  Where K is no multiple of 512 the
+// last scales are, too: K = 4224, 3% more work, takes 302 us.  Eight wavefronts of 128 x 64 products
+// read 1.5 times as much from LDS.
+//
+// With SiTU 33 registers spill (136 bytes a lane), and the activation is not covered by the next item's
+// products: 8 experts x 4096 rows, N = 1792, K = 4096 take 365 us where the same products without it
+// take 265; 32768 rows, N = 1024, K = 2048 145 and 94.
 // ---------------------------------------------------------------------------------------
 constexpr int kWaitLds = 0xC07F;                       // s_waitcnt for LDS reads alone
 constexpr int kMxTile = 256, kMxWaves = 4, kMxThreads = kMxWaves * 64;

@@ -49,7 +49,10 @@ inline bool mx_wide(const MxSizes& s) {
 //     1.1 rows, N = 384 with SiTU, K = 3584  112 / 77 / 76 / 85 / 83 / 72;
 //   few items: 8 experts x 32 rows, N = K = 4096  26 / 24 / 24 / 18 / 24 / 28; one expert, N = K =
 //     7168, 512 rows  52 / 46 / 36 / 36 / 52 / 81, 64 rows  34 / 34 / 33 / 21 / 15 / 17, 16 rows
-//     33 / 29 / 28 / 18 / 13 / 13.
+//     33 / 29 / 28 / 18 / 13 / 13;
+//   rows that all fall on one of 896 experts, which the host does not know and the rule takes for few
+//     rows each: N = 384 with SiTU, K = 3584, 16384 rows 60 us (called with one expert 53), 4096 rows
+//     37 (23).
 inline MxTiles mx_tiles(const MxSizes& s) {
   const int64_t R = s.R, E = s.E, some = std::min(R, E), few = s.cus * 3 / 4;
   auto items = [&](int tile, int block) { return (some + R / tile) * ((s.Nw + block - 1) / block); };
