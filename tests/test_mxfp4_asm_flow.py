@@ -5,6 +5,7 @@ between a product and any other instruction that reads or overwrites its result 
 what gfx950 takes for these (4 passes) and what its compiler puts behind the same instruction's
 builtin.  That rule is looked up by compiling the builtin, not taken from here."""
 
+import functools
 import re
 import subprocess
 
@@ -122,11 +123,22 @@ def hazards(code):
     return bad
 
 
-def _assembly(source, *flags):
-    r = subprocess.run([b.HIPCC, *b.COMMON_FLAGS, "--cuda-device-only", "-S", *flags, source, "-o", "-"],
+@functools.lru_cache(maxsize=None)
+def _text(source):
+    r = subprocess.run([b.HIPCC, *b.COMMON_FLAGS, "--cuda-device-only", "-S", source, "-o", "-"],
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
-    return kernels(r.stdout)
+    return r.stdout
+
+
+def _assembly(source):
+    return kernels(_text(source))
+
+
+def scratch(text):
+    """{kernel name: bytes of scratch a lane}"""
+    return {m.group(1): int(m.group(2)) for m in re.finditer(
+        r"\.amdhsa_kernel (\w+).*?\.amdhsa_private_segment_fixed_size (\d+)", text, re.S)}
 
 
 MFMA = ("v_mfma_scale_f32_16x16x128_f8f6f4", ["a[0:3]", "v[0:3]", "v[4:7]", "a[0:3]", "v8", "v9"], True)
@@ -196,3 +208,12 @@ def test_the_written_out_products_have_their_waits_on_every_path():
         assert n >= 480
         assert sum(len(to) for _, to in _blocks(code)) > 40
         assert not hazards(code), (name, hazards(code)[:5])
+
+
+@pytest.mark.slow
+def test_only_the_activation_spills_and_no_more_than_is_known():
+    """33 registers of the large tiles with the activation; the plain ones none."""
+    found = scratch(_text(f"{b.CSRC}/grouped_mxfp4_big.hip"))
+    assert len(found) == 2
+    for name, size in found.items():
+        assert size <= (136 if "ILb1E" in name else 0), name
