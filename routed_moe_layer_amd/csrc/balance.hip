@@ -387,13 +387,13 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a) {
   const double n = a.tokens[0];
   const bool some = n > 0.0 && all > 0.0;              // without, NaN rows have no gradient either
   // The scale may lie far outside fp32's range where the gradient does not: half of its power of two
-  // goes to the counts (at most 2^95, so that 31 bits of counts stay below 2^127), and what then is
-  // still above 2^95 to the result.  (Far below, nothing is left of any gradient.)
+  // goes to the counts (at most 2^80, so that sums over 4096 of 31 bits stay below 2^127), and what
+  // then is still above 2^80 to the result.  (Below 2^-190 nothing is left of any gradient.)
   const double whole = some ? static_cast<double>(a.coef) * a.E / (n * all) *
                                   (a.grad_loss ? a.grad_loss[0] : 1.0f)
                             : 0.0;
-  const int power = __builtin_amdgcn_frexp_exp(whole), half = min(max(power / 2, -95), 95);
-  const int above = __builtin_amdgcn_readfirstlane(max(power - 190, 0));
+  const int power = __builtin_amdgcn_frexp_exp(whole), half = min(max(power / 2, -80), 80);
+  const int above = __builtin_amdgcn_readfirstlane(max(power - 160, 0));
   const float scale = static_cast<float>(ldexp(whole, -half - above));
 #pragma unroll
   for (int v = 0; v < V; ++v) {

@@ -62,3 +62,18 @@ def test_equal_counts_have_no_gradient_under_any_scale(E):
     for coef, g in ((3.3e38, None), (1e38, 1e30), (-1e38, 1e-30)):
         g = None if g is None else torch.tensor([g], device="cuda")
         assert torch.equal(_grad(z, None, counts, one, coef=coef, g=g), torch.zeros_like(z))
+
+
+@pytest.mark.parametrize("E", [16, 64, 896, 4096])
+def test_large_counts_that_cancel_under_a_large_scale(E):
+    """Half of the experts share every row and every count: sum p c is their count, the gradient 0, and
+    the sum on the way to it many times as large as one count."""
+    _say(f"balance cancelling counts, large scale E={E}")
+    z = torch.full((5, E), -float("inf"), device="cuda")
+    z[:, : E // 2] = 1.25
+    counts = torch.zeros(E, dtype=I32, device="cuda")
+    counts[: E // 2] = 1 << 30                         # centred: 2^29 and -2^29
+    one = torch.ones(1, dtype=I32, device="cuda")
+    for coef, g in ((3e38, 1e38), (3e38, 1e30), (1e30, 1e20)):
+        out = _grad(z, None, counts, one, coef=coef, g=torch.tensor([g], device="cuda"))
+        assert torch.equal(out, torch.zeros_like(z))
